@@ -80,7 +80,8 @@ typedef enum {
     ENTMAXKV_OP_SPARSE_ATTEND = 1,
     ENTMAXKV_OP_FULL_ENTMAX = 2,
     ENTMAXKV_OP_FULL_SOFTMAX = 3,
-    ENTMAXKV_OP_SPARSE_SOFTMAX = 4
+    ENTMAXKV_OP_SPARSE_SOFTMAX = 4,
+    ENTMAXKV_OP_WINDOW_SOFTMAX = 5
 } entmaxkv_op;
 
 /*
@@ -306,6 +307,31 @@ ENTMAXKV_API int entmaxkv_sparse_softmax_attend(const entmaxkv_pool* pool, const
                                    const int32_t* seq_lens, int32_t B, const int32_t* sel,
                                    const int32_t* sel_count, int32_t k_max, float scale, float* out,
                                    void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * Softmax decode over a sliding window with sinks: each sequence attends to
+ * its newest `window` tokens (the last appended one included) and to its first
+ * `sinks` tokens, which stay visible when the window has moved past them.
+ *   With L = seq_lens[b], head h of kv head g, over the tokens i with i < sinks
+ *   or i >= L - window (0 <= i < L, each once):
+ *     out[b][h] = sum_i softmax(scale * q_h . k_i)_i v_i, [B][H_q][d] fp32,
+ *     lse_out[b][h] = log sum_i exp(scale * q_h . k_i), [B][H_q] fp32 (may be
+ *     NULL; natural logarithm).  A head with no token gets out = 0 and
+ *     lse = -INFINITY.
+ *   window >= 1, sinks >= 0.  Page-table entries of pages that hold none of
+ *   these tokens are never read (they may be -1, as entmaxkv_free_pages leaves
+ *   them), nor are masked tokens' values used, whatever they hold.
+ *   Sums are fp32 and taken in an order fixed by the arguments: the same call
+ *   gives the same bits.
+ *   out and lse_out may be pinned host memory, as for the other attention calls.
+ *   workspace: entmaxkv_workspace_size(ENTMAXKV_OP_WINDOW_SOFTMAX, ...) bytes
+ *   (k_max ignored).
+ */
+ENTMAXKV_API int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const float* q, int32_t H_q,
+                                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                   int32_t B, int32_t window, int32_t sinks, float scale, float* out,
+                                   float* lse_out, void* workspace, size_t ws_bytes, int32_t* status,
+                                   void* stream);
 
 /*
  * Bytes of device workspace an entry point needs (host only; uses the SM

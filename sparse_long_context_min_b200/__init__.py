@@ -11,5 +11,5 @@ workloads (``workloads``).
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
     Pool, EntmaxKVError, append_metadata, score_pages, select, sparse_attend, full_entmax_decode,
-    full_softmax_decode, workspace_size, status_string, selftest_timeout,
+    full_softmax_decode, window_softmax_decode, workspace_size, status_string, selftest_timeout,
 )

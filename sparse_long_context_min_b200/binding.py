@@ -21,7 +21,8 @@ STATIC_SCRATCH_BYTES = 16 << 20
 F32, BF16 = 0, 1
 SCORE_BBOX, SCORE_GAUSS = 0, 1
 SELECT_TOPK, SELECT_GAUSS = 0, 1
-OP_SELECT, OP_SPARSE_ATTEND, OP_FULL_ENTMAX, OP_FULL_SOFTMAX, OP_SPARSE_SOFTMAX = range(5)
+OP_SELECT, OP_SPARSE_ATTEND, OP_FULL_ENTMAX, OP_FULL_SOFTMAX, OP_SPARSE_SOFTMAX, \
+    OP_WINDOW_SOFTMAX = range(6)
 
 # every symbol the header declares (checked by the tests)
 SYMBOLS = (
@@ -29,6 +30,7 @@ SYMBOLS = (
     "entmaxkv_full_entmax_decode", "entmaxkv_full_softmax_decode", "entmaxkv_workspace_size",
     "entmaxkv_status_string", "entmaxkv_selftest_timeout", "entmaxkv_sparse_attend_static",
     "entmaxkv_sparse_softmax_attend", "entmaxkv_append_score_pages",
+    "entmaxkv_window_softmax_decode",
 )
 
 
@@ -73,6 +75,7 @@ def lib():
         L.entmaxkv_selftest_timeout.argtypes = [ctypes.c_int64, P, P]
         L.entmaxkv_sparse_attend_static.argtypes = [PP, P, I, P, I, P, I, P, P, I, F, F, P, P, P, P, P]
         L.entmaxkv_append_score_pages.argtypes = [PP, P, P, I, P, I, P, I, P, I, F, P, P, P]
+        L.entmaxkv_window_softmax_decode.argtypes = [PP, P, I, P, I, P, I, I, I, F, P, P, P, S, P, P]
         for name in SYMBOLS:
             if name not in ("entmaxkv_workspace_size", "entmaxkv_status_string"):
                 getattr(L, name).restype = ctypes.c_int
@@ -380,6 +383,27 @@ def sparse_softmax_attend(pool, q, page_table, seq_lens, sel, sel_count, scale, 
                                                 _p(seq_lens), B, _p(sel), _p(sel_count), k_max, scale,
                                                 _p(out), _p(workspace), _bytes(workspace),
                                                 _p(status), _stream(stream)), a.where)
+
+
+def window_softmax_decode(pool, q, page_table, seq_lens, window, sinks, scale, out, workspace, status, lse_out=None,
+                          stream=None):
+    """Softmax over each sequence's newest `window` tokens and its first `sinks`
+    tokens (workspace: OP_WINDOW_SOFTMAX); lse_out [B, H_q] is optional."""
+    a = _Args("window_softmax_decode")
+    B, H_q = _query(a, pool, q)
+    max_pages = _table(a, page_table, seq_lens, B)
+    a.need(out, "out", F32T, B * H_q * pool.d)
+    if lse_out is not None:
+        a.need(lse_out, "lse_out", F32T, B * H_q)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    if not (1 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31):
+        a.fail("window must be at least 1 and sinks at least 0, both below 2^31, not %r and %r" % (window, sinks))
+    a.reachable()
+    _check(lib().entmaxkv_window_softmax_decode(pool.c, _p(q), H_q, _p(page_table), max_pages, _p(seq_lens), B,
+                                                int(window), int(sinks), scale, _p(out), _p(lse_out),
+                                                _p(workspace), _bytes(workspace), _p(status), _stream(stream)),
+           a.where)
 
 
 def selftest_timeout(limit_ns, status, stream=None):

@@ -2,11 +2,13 @@
 // workspace layout, TMA descriptors, and dispatch to the kernels.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "range.cuh"
 
 namespace ekv {
 
@@ -289,6 +291,69 @@ static int attend_common(int op, const entmaxkv_pool* pool, const float* q, int 
     return launch_entmax_attend(*pool, a, B, &kmap, &vmap, st);
 }
 
+// ------------------------------------------------------------------ token ranges
+struct RangeLayout {
+    int C;
+    size_t part_o, part_ml, span, total;
+};
+
+// CTAs of a range kernel: two an SM.  Partials have a slot for each (CTA,
+// unit) pair of the staircase.
+static RangeLayout range_layout(int B, int H_q, int H_kv, int d)
+{
+    RangeLayout L{};
+    L.C = 2 * num_sms();
+    const size_t units = (size_t)B * H_kv, rows = (units + L.C) * (H_q / H_kv);
+    size_t off = 0;
+    L.part_o = off;
+    off += round256(rows * d * sizeof(float));
+    L.part_ml = off;
+    off += round256(rows * 2 * sizeof(float));
+    L.span = off;
+    off += round256(units * sizeof(int2));
+    L.total = off;
+    return L;
+}
+
+static int range_check(const entmaxkv_pool* pool, const float* q, int H_q, const int32_t* page_table, int max_pages,
+                       const int32_t* seq_lens, int B, float scale, const float* out, const int32_t* status)
+{
+    int rc = check_pool(pool, true, false);
+    if (rc) return rc;
+    if ((rc = check_heads(H_q, pool->H_kv))) return rc;
+    if (B < 0 || max_pages <= 0) return ENTMAXKV_INVALID_ARG;
+    if ((long long)max_pages * pool->ps > INT32_MAX - 64 || (long long)B * H_q > INT32_MAX)
+        return ENTMAXKV_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return ENTMAXKV_INVALID_ARG;
+    if (B == 0) return ENTMAXKV_OK;
+    if (!q || !page_table || !seq_lens || !out || !status) return ENTMAXKV_INVALID_ARG;
+    return ENTMAXKV_OK;
+}
+
+static RangeArgs range_args(const entmaxkv_pool& pool, const float* q, int H_q, const int32_t* page_table,
+                            int max_pages, const int32_t* seq_lens, int B, float scale, float* out, float* lse_out,
+                            char* ws, const RangeLayout& lay, int32_t* status)
+{
+    RangeArgs a{};
+    a.q = q;
+    a.H_q = H_q;
+    a.H_kv = pool.H_kv;
+    a.G = H_q / pool.H_kv;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.num_phys = pool.num_phys_pages;
+    a.xscale = scale * kLog2e;
+    a.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+    a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml);
+    a.span = reinterpret_cast<int2*>(ws + lay.span);
+    a.out = out;
+    a.lse = lse_out;
+    a.status = status;
+    return a;
+}
+
 }  // namespace ekv
 
 using namespace ekv;
@@ -421,11 +486,41 @@ int entmaxkv_sparse_softmax_attend(const entmaxkv_pool* pool, const float* q, in
                          sel_count, k_max, 1.5f, scale, out, nullptr, nullptr, workspace, ws_bytes, status, stream);
 }
 
+int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const float* q, int32_t H_q, const int32_t* page_table,
+                                   int32_t max_pages, const int32_t* seq_lens, int32_t B, int32_t window,
+                                   int32_t sinks, float scale, float* out, float* lse_out, void* workspace,
+                                   size_t ws_bytes, int32_t* status, void* stream)
+{
+    int rc = range_check(pool, q, H_q, page_table, max_pages, seq_lens, B, scale, out, status);
+    if (rc) return rc;
+    if (window < 1 || sinks < 0) return ENTMAXKV_INVALID_ARG;
+    if (B == 0) return ENTMAXKV_OK;
+    const RangeLayout lay = range_layout(B, H_q, pool->H_kv, pool->d);
+    if (!workspace || ws_bytes < lay.total || !aligned16(workspace)) return ENTMAXKV_WORKSPACE;
+    RangeArgs a = range_args(*pool, q, H_q, page_table, max_pages, seq_lens, B, scale, out, lse_out,
+                             static_cast<char*>(workspace), lay, status);
+    a.window = window;
+    a.sinks = sinks;
+    a.direct = 1;
+    CUtensorMap kmap, vmap;
+    if (pool->dtype == ENTMAXKV_BF16) {
+        if ((rc = make_pool_map(&kmap, *pool, pool->k_pool))) return rc;
+        if ((rc = make_pool_map(&vmap, *pool, pool->v_pool))) return rc;
+    }
+    // no more CTAs than the longest possible ranges have tiles
+    const long long pages = std::min((long long)max_pages, ((long long)sinks + pool->ps - 1) / pool->ps +
+                                                               ((long long)window + pool->ps - 1) / pool->ps + 1);
+    const long long tiles = (pages * pool->ps + kRangeTile - 1) / kRangeTile * B * pool->H_kv;
+    return launch_window(*pool, a, (int)std::min((long long)lay.C, tiles), &kmap, &vmap,
+                         static_cast<cudaStream_t>(stream));
+}
+
 size_t entmaxkv_workspace_size(int32_t op, int32_t B, int32_t H_q, int32_t H_kv, int32_t max_pages, int32_t k_max,
                                int32_t ps, int32_t d)
 {
     if (B <= 0 || H_q <= 0 || H_kv <= 0 || max_pages <= 0 || ps <= 0 || d <= 0) return 0;
     if (op == ENTMAXKV_OP_SELECT) return 0;
+    if (op == ENTMAXKV_OP_WINDOW_SOFTMAX) return range_layout(B, H_q, H_kv, d).total;
     if (is_sparse(op) && k_max <= 0) return 0;
     if (!is_sparse(op) && op != ENTMAXKV_OP_FULL_ENTMAX && op != ENTMAXKV_OP_FULL_SOFTMAX) return 0;
     return attn_layout(op, B, H_q, H_kv, max_pages, k_max, ps, d).total;

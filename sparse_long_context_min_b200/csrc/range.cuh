@@ -1,0 +1,155 @@
+// Softmax decode attention over token ranges: what the sliding-window kernels
+// and the shared-prefix kernels have in common (internal to the library).
+//
+// Work is cut into units (the rows that read one key/value range through one
+// kv head) of 64-token tiles.  The tiles of all units, laid end to end, are
+// dealt to the CTAs in equal consecutive shares, so every CTA streams the same
+// number of bytes whatever the lengths of the sequences; a share that starts or
+// ends inside a unit leaves a partial result (o, running maximum, sum) that a
+// merge kernel joins.  (CTA c, unit u) pairs form a monotone staircase, so
+// c + u names a partial's slot uniquely.
+#pragma once
+
+#include "common.cuh"
+
+namespace ekv {
+
+constexpr int kRangeTile = 64;           // tokens of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct RangeArgs {
+    const float* q;                // [B][H_q][d]
+    int H_q, H_kv, G;
+    const int32_t* page_table;     // [B][max_pages]
+    int max_pages;
+    const int32_t* seq_lens;       // [B]
+    int B;
+    int num_phys;
+    int window, sinks;             // window form: tokens < sinks and >= L - window
+    const int32_t* shared;         // [B] prefix form: first page of each sequence's own range, else NULL
+    float xscale;                  // scale * log2(e): scores are kept in the base-2 domain
+    float* part_o;                 // [CTAs + units][G][d] partial outputs
+    float* part_ml;                // [CTAs + units][G][2] running maximum (base 2) and sum
+    int2* span;                    // [units] first and last CTA of a unit
+    float* out;                    // [B][H_q][d]
+    float* lse;                    // [B][H_q] or NULL
+    int32_t* status;
+    int direct;                    // write finished units straight to out
+};
+
+// The kernels over each sequence's range (window.cu), C CTAs.
+int launch_range(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
+                 const CUtensorMap* vmap, cudaStream_t stream);
+// The same, and the merge of units that CTAs share.
+int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
+                  const CUtensorMap* vmap, cudaStream_t stream);
+
+// The pages a sequence's unit walks: logical pages [0, n1) and [p2, P), tokens
+// valid where pos < s or w0 <= pos < L.
+struct SeqSpan {
+    int L, s, w0, n1, p2, P;
+    EKV_DEV int pages() const { return n1 + P - p2; }
+    EKV_DEV int tiles(int ps) const { return (int)(((long long)pages() * ps + kRangeTile - 1) / kRangeTile); }
+    EKV_DEV int logical(int i) const { return i < n1 ? i : p2 + i - n1; }
+    EKV_DEV bool valid(int pos) const { return pos < L && (pos < s || pos >= w0); }
+};
+
+EKV_DEV SeqSpan seq_span(const RangeArgs& a, int b, int ps, bool rep)
+{
+    SeqSpan r;
+    r.L = max(a.seq_lens[b], 0);
+    r.P = (int)(((long long)r.L + ps - 1) / ps);
+    if (r.P > a.max_pages) {
+        if (rep) report(a.status, ENTMAXKV_DEVICE_BOUNDS);
+        r.P = a.max_pages;
+    }
+    if (a.shared) {
+        r.s = 0;
+        r.n1 = 0;
+        r.p2 = min(a.shared[b], r.P);
+        r.w0 = r.p2 * ps;
+    } else {
+        r.s = min(a.sinks, r.L);
+        r.w0 = max(r.s, r.L - a.window);
+        r.n1 = min((r.s + ps - 1) / ps, r.P);
+        r.p2 = min(max(r.w0 / ps, r.n1), r.P);
+    }
+    return r;
+}
+
+// A CTA's share of the tiles: starts at tile t of unit (b, g), `left` tiles;
+// C is the number of CTAs that have a share (each at least one tile).
+struct RangeWalk {
+    int b, g, t, C;
+    long long left, total;
+};
+
+// All threads of the block call.
+EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
+{
+    __shared__ long long wsum[32];
+    __shared__ int at[3];
+    const int tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = n >> 5;
+    RangeWalk w;
+    long long mine = 0;
+    int first = 0;                                     // tiles of sequence tid (the first chunk)
+    for (int b = tid; b < a.B; b += n) {
+        const int t = seq_span(a, b, ps, c == 0).tiles(ps);
+        if (b == tid) first = t;
+        mine += t;
+    }
+    const long long sum = warp_sum(mine);
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < nw; ++i) total += wsum[i];
+    total *= a.H_kv;
+    const int C = (int)min((long long)grid, total);
+    w.total = total;
+    w.C = C;
+    w.left = 0;
+    w.b = w.g = w.t = 0;
+    if (c >= C) return w;
+    const long long t0 = total * c / C;
+    w.left = total * (c + 1) / C - t0;
+    // the sequence that holds tile t0: chunks of blockDim sequences in turn
+    long long before = 0;
+    for (int base = 0; base < a.B; base += n) {
+        const int b = base + tid;
+        const int t = base == 0 ? first : (b < a.B ? seq_span(a, b, ps, false).tiles(ps) : 0);
+        long long inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[warp] = inc;
+        if (tid == 0) at[0] = -1;
+        __syncthreads();
+        long long off = before + inc - t, chunk = 0;
+        for (int i = 0; i < nw; ++i) {
+            if (i < warp) off += wsum[i];
+            chunk += wsum[i];
+        }
+        const long long in = t0 - off * a.H_kv;        // tile t0 within this sequence's units
+        if (t > 0 && in >= 0 && in < (long long)t * a.H_kv) {
+            at[0] = b;
+            at[1] = (int)(in / t);
+            at[2] = (int)(in % t);
+        }
+        __syncthreads();
+        if (at[0] >= 0) break;
+        before += chunk;
+    }
+    w.b = at[0];
+    w.g = at[1];
+    w.t = at[2];
+    return w;
+}
+
+// The CTA whose share holds tile `at` of all tiles.
+EKV_DEV int range_cta_of(long long at, long long total, int C) { return (int)(((at + 1) * C - 1) / total); }
+
+}  // namespace ekv
