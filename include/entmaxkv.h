@@ -24,7 +24,7 @@
  *   launched by that call, except for ENTMAXKV_CUDA_ERROR where a launch may
  *   have failed part way.
  * - `status` (device, one int32): errors found by the kernels themselves
- *   (ENTMAXKV_TIMEOUT, ENTMAXKV_DEVICE_BOUNDS) are written there with an
+ *   (ENTMAXKV_TIMEOUT, ENTMAXKV_DEVICE_BOUNDS, ENTMAXKV_NO_PAGES) are written there with an
  *   atomic compare-and-swap from 0, so the first error sticks.  The library
  *   never clears it: the caller zeroes it, runs its step, and reads it after
  *   synchronising.  A kernel that reports an error skips the offending access
@@ -69,7 +69,8 @@ typedef enum {
     ENTMAXKV_TIMEOUT = 4,        /* a bounded device wait ran out (device status) */
     ENTMAXKV_DEVICE_BOUNDS = 5,  /* a page id or index failed its device check */
     ENTMAXKV_WORKSPACE = 6,      /* workspace pointer NULL or ws_bytes too small */
-    ENTMAXKV_STATIC_LIMIT = 7    /* needs more scratch than the built-in buffer holds */
+    ENTMAXKV_STATIC_LIMIT = 7,   /* needs more scratch than the built-in buffer holds */
+    ENTMAXKV_NO_PAGES = 8        /* the pool had too few free pages (device status) */
 } entmaxkv_status;
 
 typedef enum { ENTMAXKV_F32 = 0, ENTMAXKV_BF16 = 1 } entmaxkv_dtype;
@@ -81,7 +82,9 @@ typedef enum {
     ENTMAXKV_OP_FULL_ENTMAX = 2,
     ENTMAXKV_OP_FULL_SOFTMAX = 3,
     ENTMAXKV_OP_SPARSE_SOFTMAX = 4,
-    ENTMAXKV_OP_WINDOW_SOFTMAX = 5
+    ENTMAXKV_OP_WINDOW_SOFTMAX = 5,
+    ENTMAXKV_OP_PREFIX_SOFTMAX = 6,
+    ENTMAXKV_OP_PAGES = 7
 } entmaxkv_op;
 
 /*
@@ -332,6 +335,99 @@ ENTMAXKV_API int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const
                                    int32_t B, int32_t window, int32_t sinks, float scale, float* out,
                                    float* lse_out, void* workspace, size_t ws_bytes, int32_t* status,
                                    void* stream);
+
+/*
+ * Page management
+ * ---------------
+ * The calls below keep page tables and one reference count per physical page,
+ * so that sequences can share pages, on the device and in stream order: nothing
+ * is read back, and all of them can be captured into a graph.
+ *   ref        : [num_phys_pages] int32, the number of page-table entries that
+ *                name the page; 0 = free.  Zeroed by the caller at the start.
+ *   page_table : [B][max_pages] int32; -1 (any negative value) where a row holds
+ *                no page.  The caller fills it with -1 at the start.
+ *   seq_lens   : [B] int32.
+ * Every entry >= 0 of the table is one reference; entries beyond a row's length
+ * may hold pages reserved for tokens to come.  New pages are the lowest-numbered
+ * free pages, handed out in ascending order, so a call's result depends on its
+ * inputs alone.  Calls that share a table, counts or a workspace run in stream
+ * order; B * max_pages < 2^31.
+ *   workspace: entmaxkv_workspace_size(ENTMAXKV_OP_PAGES, B, 0, 0, 0, k_max, 0, 0)
+ *   bytes with k_max = num_phys_pages and B = the table's rows (0 for
+ *   entmaxkv_copy_pages and entmaxkv_compact_pages suffices).  Scratch, as for
+ *   the attention calls.
+ * Errors the kernels find go to *status: ENTMAXKV_DEVICE_BOUNDS for a row, page
+ * or length out of range, for a refused pair, or for a count that does not
+ * cover the table's entries; ENTMAXKV_NO_PAGES.
+ */
+
+/*
+ * Copy pages inside the pool: page dst[i] becomes page src[i] -- keys, values,
+ * kmin, kmax, mean, m2 and count -- for i < n (src, dst: [n] int32).  All copies
+ * happen at once: a page may be read by several pairs, but a pair whose dst is
+ * another pair's dst or any other pair's src is refused (skipped and reported);
+ * src[i] == dst[i] copies nothing.  Tables and counts are not touched.
+ */
+ENTMAXKV_API int entmaxkv_copy_pages(const entmaxkv_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                        void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * Fork sequences: row dst[i] becomes a copy of row src[i] for i < n (src, dst:
+ * [n] int32, n <= B; e.g. the beams or samples that continue a prompt).  What
+ * the destination held is released first.  Pages that the source fills are
+ * shared (their counts grow); the page that it ends inside of is copied to a
+ * new page, so that both can append; pages reserved beyond its length stay with
+ * the source.  Entries of the source without a page (entmaxkv_free_pages with a
+ * window) stay without one.  seq_lens[dst] = seq_lens[src].
+ *   A source may be listed many times.  A pair whose dst is listed twice or is
+ *   any pair's source is refused: skipped and reported, its rows as they were.
+ *   When the pool runs out of pages the forks served last are left empty
+ *   (length 0, no pages) and ENTMAXKV_NO_PAGES is reported.
+ */
+ENTMAXKV_API int entmaxkv_fork_sequences(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table,
+                            int32_t max_pages, int32_t* seq_lens, int32_t B, const int32_t* src,
+                            const int32_t* dst, int32_t n, void* workspace, size_t ws_bytes, int32_t* status,
+                            void* stream);
+
+/*
+ * Free pages of the listed rows (rows: [n] int32; NULL with n = B: every row; a
+ * row listed twice is freed once).
+ *   window < 0 : the sequence ends: every entry is released and the row's length
+ *     becomes 0.
+ *   window >= 0: only the pages go that entmaxkv_window_softmax_decode with this
+ *     window and `sinks` no longer reads, now or after further appends: those
+ *     with no token < sinks and no token >= seq_lens - window.  Lengths stay.
+ * Released entries become -1.  A page is free when its last reference is gone.
+ * No workspace.
+ */
+ENTMAXKV_API int entmaxkv_free_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table,
+                        int32_t max_pages, int32_t* seq_lens, int32_t B, const int32_t* rows, int32_t n,
+                        int32_t window, int32_t sinks, int32_t* status, void* stream);
+
+/*
+ * Reserve pages: row b gets room for lens[b] tokens in all ([B] int32; what
+ * entmaxkv_append_metadata asks of the table before an append of n_new tokens is
+ * lens = seq_lens + n_new).  Entries from page ceil(seq_lens / ps) up to
+ * ceil(lens / ps) that hold no page get one; rows are served in order.  When too
+ * few pages are free, the first row that cannot be served in full and all later
+ * rows that want pages get none (ENTMAXKV_NO_PAGES).  A row whose lens exceeds
+ * max_pages * ps gets none (ENTMAXKV_DEVICE_BOUNDS).
+ */
+ENTMAXKV_API int entmaxkv_reserve_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table,
+                           int32_t max_pages, const int32_t* seq_lens, int32_t B, const int32_t* lens,
+                           void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * Compact the pool: afterwards the pages in use are exactly [0, live), and
+ * *live (device, one int32) says how many.  The i-th free page below `live`
+ * receives the i-th used page at or above it (both ascending), with its count;
+ * the table's entries follow.  The pages moved away from are free, their
+ * contents left as they were.  Every table that names pages of the pool has to
+ * be part of the call (B rows; B = 0 only moves pages and counts).
+ */
+ENTMAXKV_API int entmaxkv_compact_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table,
+                           int32_t max_pages, int32_t B, int32_t* live, void* workspace, size_t ws_bytes,
+                           int32_t* status, void* stream);
 
 /*
  * Bytes of device workspace an entry point needs (host only; uses the SM

@@ -16,13 +16,13 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libentmaxkv.so")
 
-OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, TIMEOUT, DEVICE_BOUNDS, WORKSPACE, STATIC_LIMIT = range(8)
+OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, TIMEOUT, DEVICE_BOUNDS, WORKSPACE, STATIC_LIMIT, NO_PAGES = range(9)
 STATIC_SCRATCH_BYTES = 16 << 20
 F32, BF16 = 0, 1
 SCORE_BBOX, SCORE_GAUSS = 0, 1
 SELECT_TOPK, SELECT_GAUSS = 0, 1
 OP_SELECT, OP_SPARSE_ATTEND, OP_FULL_ENTMAX, OP_FULL_SOFTMAX, OP_SPARSE_SOFTMAX, \
-    OP_WINDOW_SOFTMAX = range(6)
+    OP_WINDOW_SOFTMAX, OP_PREFIX_SOFTMAX, OP_PAGES = range(8)
 
 # every symbol the header declares (checked by the tests)
 SYMBOLS = (
@@ -30,7 +30,8 @@ SYMBOLS = (
     "entmaxkv_full_entmax_decode", "entmaxkv_full_softmax_decode", "entmaxkv_workspace_size",
     "entmaxkv_status_string", "entmaxkv_selftest_timeout", "entmaxkv_sparse_attend_static",
     "entmaxkv_sparse_softmax_attend", "entmaxkv_append_score_pages",
-    "entmaxkv_window_softmax_decode",
+    "entmaxkv_window_softmax_decode", "entmaxkv_copy_pages", "entmaxkv_fork_sequences", "entmaxkv_free_pages",
+    "entmaxkv_reserve_pages", "entmaxkv_compact_pages",
 )
 
 
@@ -76,6 +77,11 @@ def lib():
         L.entmaxkv_sparse_attend_static.argtypes = [PP, P, I, P, I, P, I, P, P, I, F, F, P, P, P, P, P]
         L.entmaxkv_append_score_pages.argtypes = [PP, P, P, I, P, I, P, I, P, I, F, P, P, P]
         L.entmaxkv_window_softmax_decode.argtypes = [PP, P, I, P, I, P, I, I, I, F, P, P, P, S, P, P]
+        L.entmaxkv_copy_pages.argtypes = [PP, P, P, I, P, S, P, P]
+        L.entmaxkv_fork_sequences.argtypes = [PP, P, P, I, P, I, P, P, I, P, S, P, P]
+        L.entmaxkv_free_pages.argtypes = [PP, P, P, I, P, I, P, I, I, I, P, P]
+        L.entmaxkv_reserve_pages.argtypes = [PP, P, P, I, P, I, P, P, S, P, P]
+        L.entmaxkv_compact_pages.argtypes = [PP, P, P, I, I, P, P, S, P, P]
         for name in SYMBOLS:
             if name not in ("entmaxkv_workspace_size", "entmaxkv_status_string"):
                 getattr(L, name).restype = ctypes.c_int
@@ -404,6 +410,93 @@ def window_softmax_decode(pool, q, page_table, seq_lens, window, sinks, scale, o
                                                 int(window), int(sinks), scale, _p(out), _p(lse_out),
                                                 _p(workspace), _bytes(workspace), _p(status), _stream(stream)),
            a.where)
+
+
+def _owned(a, pool, ref, page_table, seq_lens):
+    """A reference-counted table: ref [num_phys], page_table [B, max_pages] and
+    seq_lens [B] (None where the call takes none), int32; returns (B, max_pages)."""
+    a.need(ref, "ref", I32, pool.num_phys)
+    a.need(page_table, "page_table", I32, dims=2)
+    B, max_pages = page_table.shape
+    if seq_lens is not None:
+        a.need(seq_lens, "seq_lens", I32, B)
+    return B, max_pages
+
+
+def _pairs(a, src, dst):
+    """src and dst, int32 lists of one length; returns it."""
+    a.need(src, "src", I32, dims=1)
+    a.need(dst, "dst", I32, dims=1)
+    if src.shape[0] != dst.shape[0]:
+        a.fail("src lists %d entries, dst %d" % (src.shape[0], dst.shape[0]))
+    return src.shape[0]
+
+
+def copy_pages(pool, src, dst, workspace, status, stream=None):
+    """Page dst[i] becomes page src[i], keys, values and metadata (workspace: OP_PAGES)."""
+    a = _Args("copy_pages")
+    n = _pairs(a, src, dst)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    a.reachable()
+    _check(lib().entmaxkv_copy_pages(pool.c, _p(src), _p(dst), n, _p(workspace), _bytes(workspace), _p(status),
+                                     _stream(stream)), a.where)
+
+
+def fork_sequences(pool, ref, page_table, seq_lens, src, dst, workspace, status, stream=None):
+    """Row dst[i] of the table becomes a copy of row src[i]: full pages shared,
+    the page it ends inside of copied (workspace: OP_PAGES)."""
+    a = _Args("fork_sequences")
+    B, max_pages = _owned(a, pool, ref, page_table, seq_lens)
+    n = _pairs(a, src, dst)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    a.reachable()
+    _check(lib().entmaxkv_fork_sequences(pool.c, _p(ref), _p(page_table), max_pages, _p(seq_lens), B, _p(src), _p(dst),
+                                         n, _p(workspace), _bytes(workspace), _p(status), _stream(stream)), a.where)
+
+
+def free_pages(pool, ref, page_table, seq_lens, rows, status, window=None, sinks=0, stream=None):
+    """Release every page of the listed rows (rows None: all) and empty them; or,
+    with a window, only the pages behind it and after the sinks."""
+    a = _Args("free_pages")
+    B, max_pages = _owned(a, pool, ref, page_table, seq_lens)
+    n = B
+    if rows is not None:
+        a.need(rows, "rows", I32, dims=1)
+        n = rows.shape[0]
+    a.need(status, "status", I32, 1)
+    if window is not None and not 0 <= window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
+        a.fail("window and sinks must be at least 0 and below 2^31, not %r and %r" % (window, sinks))
+    a.reachable()
+    _check(lib().entmaxkv_free_pages(pool.c, _p(ref), _p(page_table), max_pages, _p(seq_lens), B, _p(rows), n,
+                                     -1 if window is None else int(window), int(sinks), _p(status),
+                                     _stream(stream)), a.where)
+
+
+def reserve_pages(pool, ref, page_table, seq_lens, lens, workspace, status, stream=None):
+    """Give every row pages for lens[b] tokens in all (workspace: OP_PAGES)."""
+    a = _Args("reserve_pages")
+    B, max_pages = _owned(a, pool, ref, page_table, seq_lens)
+    a.need(lens, "lens", I32, B)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    a.reachable()
+    _check(lib().entmaxkv_reserve_pages(pool.c, _p(ref), _p(page_table), max_pages, _p(seq_lens), B, _p(lens),
+                                        _p(workspace), _bytes(workspace), _p(status), _stream(stream)), a.where)
+
+
+def compact_pages(pool, ref, page_table, live, workspace, status, stream=None):
+    """Move the used pages to [0, live) and rename the table's entries; live is a
+    one-element int32 result (workspace: OP_PAGES)."""
+    a = _Args("compact_pages")
+    B, max_pages = _owned(a, pool, ref, page_table, None)
+    a.need(live, "live", I32, 1)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    a.reachable()
+    _check(lib().entmaxkv_compact_pages(pool.c, _p(ref), _p(page_table), max_pages, B, _p(live), _p(workspace),
+                                        _bytes(workspace), _p(status), _stream(stream)), a.where)
 
 
 def selftest_timeout(limit_ns, status, stream=None):

@@ -354,6 +354,27 @@ static RangeArgs range_args(const entmaxkv_pool& pool, const float* q, int H_q, 
     return a;
 }
 
+// ------------------------------------------------------------------ pages
+// The pool and the table of a page-management call.  `entries`: rows of the
+// workspace; 0 with a NULL workspace where the call needs none.
+static int pages_check(const entmaxkv_pool* pool, int max_pages, int B)
+{
+    int rc = check_pool(pool, true, true);
+    if (rc) return rc;
+    if (B < 0 || max_pages <= 0) return ENTMAXKV_INVALID_ARG;
+    // 32-bit counts of table entries and of a page's bytes, and the bitmap of
+    // the counting cluster (200 KB in each of its 8 CTAs)
+    if ((long long)B * max_pages > INT32_MAX || pool->H_kv > 65535 || pool->num_phys_pages > 13000000)
+        return ENTMAXKV_UNSUPPORTED;
+    return ENTMAXKV_OK;
+}
+
+static int pages_ws_check(const entmaxkv_pool& pool, int entries, const void* workspace, size_t ws_bytes)
+{
+    const size_t need = pages_workspace(entries, pool.num_phys_pages);
+    return !workspace || ws_bytes < need || !aligned16(workspace) ? ENTMAXKV_WORKSPACE : ENTMAXKV_OK;
+}
+
 }  // namespace ekv
 
 using namespace ekv;
@@ -515,9 +536,74 @@ int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const float* q, in
                          static_cast<cudaStream_t>(stream));
 }
 
+int entmaxkv_copy_pages(const entmaxkv_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                        void* workspace, size_t ws_bytes, int32_t* status, void* stream)
+{
+    int rc = pages_check(pool, 1, 0);
+    if (rc) return rc;
+    if (n < 0) return ENTMAXKV_INVALID_ARG;
+    if (n == 0) return ENTMAXKV_OK;
+    if (!src || !dst || !status) return ENTMAXKV_INVALID_ARG;
+    if ((rc = pages_ws_check(*pool, 0, workspace, ws_bytes))) return rc;
+    return launch_copy_pages(*pool, src, dst, n, static_cast<char*>(workspace), status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int entmaxkv_fork_sequences(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table, int32_t max_pages,
+                            int32_t* seq_lens, int32_t B, const int32_t* src, const int32_t* dst, int32_t n,
+                            void* workspace, size_t ws_bytes, int32_t* status, void* stream)
+{
+    int rc = pages_check(pool, max_pages, B);
+    if (rc) return rc;
+    if (n < 0 || n > B) return ENTMAXKV_INVALID_ARG;
+    if (n == 0) return ENTMAXKV_OK;
+    if (!ref || !page_table || !seq_lens || !src || !dst || !status) return ENTMAXKV_INVALID_ARG;
+    if ((rc = pages_ws_check(*pool, n, workspace, ws_bytes))) return rc;
+    return launch_fork(*pool, ref, page_table, max_pages, seq_lens, B, src, dst, n, static_cast<char*>(workspace),
+                       status, static_cast<cudaStream_t>(stream));
+}
+
+int entmaxkv_free_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table, int32_t max_pages,
+                        int32_t* seq_lens, int32_t B, const int32_t* rows, int32_t n, int32_t window, int32_t sinks,
+                        int32_t* status, void* stream)
+{
+    int rc = pages_check(pool, max_pages, B);
+    if (rc) return rc;
+    if (n < 0 || sinks < 0) return ENTMAXKV_INVALID_ARG;
+    if (n == 0 || B == 0) return ENTMAXKV_OK;
+    if (!ref || !page_table || !seq_lens || !status || (!rows && n != B)) return ENTMAXKV_INVALID_ARG;
+    return launch_free_pages(*pool, ref, page_table, max_pages, seq_lens, B, rows, n, window, sinks, status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int entmaxkv_reserve_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table, int32_t max_pages,
+                           const int32_t* seq_lens, int32_t B, const int32_t* lens, void* workspace, size_t ws_bytes,
+                           int32_t* status, void* stream)
+{
+    int rc = pages_check(pool, max_pages, B);
+    if (rc) return rc;
+    if (B == 0) return ENTMAXKV_OK;
+    if (!ref || !page_table || !seq_lens || !lens || !status) return ENTMAXKV_INVALID_ARG;
+    if ((rc = pages_ws_check(*pool, B, workspace, ws_bytes))) return rc;
+    return launch_reserve(*pool, ref, page_table, max_pages, seq_lens, B, lens, static_cast<char*>(workspace), status,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int entmaxkv_compact_pages(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table, int32_t max_pages, int32_t B,
+                           int32_t* live, void* workspace, size_t ws_bytes, int32_t* status, void* stream)
+{
+    int rc = pages_check(pool, max_pages, B);
+    if (rc) return rc;
+    if (!ref || (B > 0 && !page_table) || !live || !status) return ENTMAXKV_INVALID_ARG;
+    if ((rc = pages_ws_check(*pool, 0, workspace, ws_bytes))) return rc;
+    return launch_compact(*pool, ref, page_table, max_pages, B, live, static_cast<char*>(workspace), status,
+                          static_cast<cudaStream_t>(stream));
+}
+
 size_t entmaxkv_workspace_size(int32_t op, int32_t B, int32_t H_q, int32_t H_kv, int32_t max_pages, int32_t k_max,
                                int32_t ps, int32_t d)
 {
+    if (op == ENTMAXKV_OP_PAGES) return pages_workspace(B, k_max);
     if (B <= 0 || H_q <= 0 || H_kv <= 0 || max_pages <= 0 || ps <= 0 || d <= 0) return 0;
     if (op == ENTMAXKV_OP_SELECT) return 0;
     if (op == ENTMAXKV_OP_WINDOW_SOFTMAX) return range_layout(B, H_q, H_kv, d).total;
@@ -537,6 +623,7 @@ const char* entmaxkv_status_string(int32_t code)
         case ENTMAXKV_DEVICE_BOUNDS: return "device index check failed (page id, list entry or count out of range)";
         case ENTMAXKV_WORKSPACE: return "workspace missing, misaligned or too small";
         case ENTMAXKV_STATIC_LIMIT: return "problem needs more scratch than the built-in buffer holds";
+        case ENTMAXKV_NO_PAGES: return "the pool has no free page left";
         default: return "unknown status";
     }
 }

@@ -82,6 +82,19 @@ int attend_check(int op, const entmaxkv_pool* pool, const float* q, int H_q, con
                  int max_pages, const int32_t* seq_lens, int B, const int32_t* sel, const int32_t* sel_count,
                  int k_max, float alpha, float scale, const float* out, const int32_t* status);
 
+// page management (cache.cu); ws holds pages_workspace(entries, num_phys) bytes
+size_t pages_workspace(long long entries, long long num_phys);
+int launch_copy_pages(const entmaxkv_pool& pool, const int32_t* src, const int32_t* dst, int n, char* ws,
+                      int32_t* status, cudaStream_t stream);
+int launch_free_pages(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table, int max_pages, int32_t* seq_lens,
+                      int B, const int32_t* rows, int n, int window, int sinks, int32_t* status, cudaStream_t stream);
+int launch_fork(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table, int max_pages, int32_t* seq_lens, int B,
+                const int32_t* src, const int32_t* dst, int n, char* ws, int32_t* status, cudaStream_t stream);
+int launch_reserve(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table, int max_pages,
+                   const int32_t* seq_lens, int B, const int32_t* lens, char* ws, int32_t* status, cudaStream_t stream);
+int launch_compact(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table, int max_pages, int B, int32_t* live,
+                   char* ws, int32_t* status, cudaStream_t stream);
+
 int launch_selftest_timeout(int64_t limit_ns, int32_t* status, cudaStream_t stream);
 
 // set the dynamic shared memory limit of a kernel once per device
