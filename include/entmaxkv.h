@@ -337,6 +337,35 @@ ENTMAXKV_API int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const
                                    void* stream);
 
 /*
+ * Softmax decode of a batch whose sequences share prefixes: the tokens of a
+ * shared prefix are read once for all sequences of its group, the others for
+ * each sequence.
+ *   out[b][h] = sum_{i < L} softmax(scale * q_h . k_i)_i v_i over all L =
+ *   seq_lens[b] tokens, and lse_out, as for entmaxkv_window_softmax_decode (the
+ *   result is that of entmaxkv_full_softmax_decode up to rounding).
+ *   group_start [n_groups + 1] int32, ascending: group j is the consecutive rows
+ *     group_start[j] .. group_start[j + 1] - 1 of the batch; rows outside every
+ *     group share nothing.  Bounds out of [0, B] or descending are reported as
+ *     ENTMAXKV_DEVICE_BOUNDS and clipped.
+ *   prefix_lens [n_groups] int32: the first prefix_lens[j] tokens are the same
+ *     for the whole group, and the page-table rows of its sequences name the same
+ *     physical pages for the whole pages among them (as entmaxkv_fork_sequences
+ *     leaves them): the library reads these pages through the group's first row.
+ *     Tokens behind the last whole page, and those behind the group's shortest
+ *     non-empty sequence, are read through each sequence's own row.
+ *   0 <= n_groups <= B (0: group_start and prefix_lens may be NULL).
+ *   A sequence without tokens gets out = 0 and lse = -INFINITY.  The same call
+ *   gives the same bits.
+ *   workspace: entmaxkv_workspace_size(ENTMAXKV_OP_PREFIX_SOFTMAX, ...) bytes
+ *   (k_max ignored).
+ */
+ENTMAXKV_API int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, int32_t H_q,
+                                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                   int32_t B, const int32_t* group_start, const int32_t* prefix_lens,
+                                   int32_t n_groups, float scale, float* out, float* lse_out, void* workspace,
+                                   size_t ws_bytes, int32_t* status, void* stream);
+
+/*
  * Page management
  * ---------------
  * The calls below keep page tables and one reference count per physical page,

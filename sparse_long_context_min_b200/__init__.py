@@ -11,6 +11,6 @@ workloads (``workloads``).
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
     Pool, EntmaxKVError, append_metadata, score_pages, select, sparse_attend, full_entmax_decode,
-    full_softmax_decode, window_softmax_decode, copy_pages, fork_sequences,
-    free_pages, reserve_pages, compact_pages, workspace_size, status_string, selftest_timeout,
+    full_softmax_decode, window_softmax_decode, prefix_softmax_decode, copy_pages,
+    fork_sequences, free_pages, reserve_pages, compact_pages, workspace_size, status_string, selftest_timeout,
 )

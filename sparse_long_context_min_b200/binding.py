@@ -30,8 +30,8 @@ SYMBOLS = (
     "entmaxkv_full_entmax_decode", "entmaxkv_full_softmax_decode", "entmaxkv_workspace_size",
     "entmaxkv_status_string", "entmaxkv_selftest_timeout", "entmaxkv_sparse_attend_static",
     "entmaxkv_sparse_softmax_attend", "entmaxkv_append_score_pages",
-    "entmaxkv_window_softmax_decode", "entmaxkv_copy_pages", "entmaxkv_fork_sequences", "entmaxkv_free_pages",
-    "entmaxkv_reserve_pages", "entmaxkv_compact_pages",
+    "entmaxkv_window_softmax_decode", "entmaxkv_prefix_softmax_decode", "entmaxkv_copy_pages",
+    "entmaxkv_fork_sequences", "entmaxkv_free_pages", "entmaxkv_reserve_pages", "entmaxkv_compact_pages",
 )
 
 
@@ -77,6 +77,7 @@ def lib():
         L.entmaxkv_sparse_attend_static.argtypes = [PP, P, I, P, I, P, I, P, P, I, F, F, P, P, P, P, P]
         L.entmaxkv_append_score_pages.argtypes = [PP, P, P, I, P, I, P, I, P, I, F, P, P, P]
         L.entmaxkv_window_softmax_decode.argtypes = [PP, P, I, P, I, P, I, I, I, F, P, P, P, S, P, P]
+        L.entmaxkv_prefix_softmax_decode.argtypes = [PP, P, I, P, I, P, I, P, P, I, F, P, P, P, S, P, P]
         L.entmaxkv_copy_pages.argtypes = [PP, P, P, I, P, S, P, P]
         L.entmaxkv_fork_sequences.argtypes = [PP, P, P, I, P, I, P, P, I, P, S, P, P]
         L.entmaxkv_free_pages.argtypes = [PP, P, P, I, P, I, P, I, I, I, P, P]
@@ -410,6 +411,29 @@ def window_softmax_decode(pool, q, page_table, seq_lens, window, sinks, scale, o
                                                 int(window), int(sinks), scale, _p(out), _p(lse_out),
                                                 _p(workspace), _bytes(workspace), _p(status), _stream(stream)),
            a.where)
+
+
+def prefix_softmax_decode(pool, q, page_table, seq_lens, group_start, prefix_lens, scale, out, workspace, status,
+                          lse_out=None, stream=None):
+    """Softmax over all tokens of each sequence, those of a group's shared prefix
+    read once: group j is rows group_start[j] to group_start[j + 1] - 1, its first
+    prefix_lens[j] tokens are shared (workspace: OP_PREFIX_SOFTMAX)."""
+    a = _Args("prefix_softmax_decode")
+    B, H_q = _query(a, pool, q)
+    max_pages = _table(a, page_table, seq_lens, B)
+    a.need(prefix_lens, "prefix_lens", I32, dims=1)
+    n_groups = prefix_lens.shape[0]
+    a.need(group_start, "group_start", I32, n_groups + 1)
+    a.need(out, "out", F32T, B * H_q * pool.d)
+    if lse_out is not None:
+        a.need(lse_out, "lse_out", F32T, B * H_q)
+    a.need(workspace, "workspace")
+    a.need(status, "status", I32, 1)
+    a.reachable()
+    _check(lib().entmaxkv_prefix_softmax_decode(pool.c, _p(q), H_q, _p(page_table), max_pages, _p(seq_lens), B,
+                                                _p(group_start), _p(prefix_lens), n_groups, scale, _p(out),
+                                                _p(lse_out), _p(workspace), _bytes(workspace), _p(status),
+                                                _stream(stream)), a.where)
 
 
 def _owned(a, pool, ref, page_table, seq_lens):

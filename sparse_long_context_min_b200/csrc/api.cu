@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "prefix.cuh"
 #include "range.cuh"
 
 namespace ekv {
@@ -354,6 +355,38 @@ static RangeArgs range_args(const entmaxkv_pool& pool, const float* q, int H_q, 
     return a;
 }
 
+struct PrefixLayout {
+    RangeLayout range;
+    int C;
+    size_t shared, gid, groups, total_blocks, span, part_o, part_ml, total;
+};
+
+// Rows a unit of the prefix kernel holds, at most (its kernel for fp32 caches holds 8).
+constexpr int kPrefixRows = 128, kPrefixRowsF32 = 8;
+
+static PrefixLayout prefix_layout(int B, int H_q, int H_kv, int d)
+{
+    PrefixLayout L{};
+    L.range = range_layout(B, H_q, H_kv, d);
+    L.C = num_sms();
+    const size_t units = (size_t)H_kv * ((size_t)B * (H_q / H_kv) / kPrefixRowsF32 + B);
+    const size_t rows = (size_t)B * H_q + (size_t)L.C * kPrefixRows;
+    size_t off = L.range.total;
+    auto take = [&](size_t& at, size_t bytes) {
+        at = off;
+        off += round256(bytes);
+    };
+    take(L.shared, B * sizeof(int32_t));
+    take(L.gid, B * sizeof(int32_t));
+    take(L.groups, B * sizeof(PrefixGroup));
+    take(L.total_blocks, sizeof(long long));
+    take(L.span, units * sizeof(int2));
+    take(L.part_o, rows * d * sizeof(float));
+    take(L.part_ml, rows * 2 * sizeof(float));
+    L.total = off;
+    return L;
+}
+
 // ------------------------------------------------------------------ pages
 // The pool and the table of a page-management call.  `entries`: rows of the
 // workspace; 0 with a NULL workspace where the call needs none.
@@ -536,6 +569,44 @@ int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const float* q, in
                          static_cast<cudaStream_t>(stream));
 }
 
+int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, int32_t H_q, const int32_t* page_table,
+                                   int32_t max_pages, const int32_t* seq_lens, int32_t B, const int32_t* group_start,
+                                   const int32_t* prefix_lens, int32_t n_groups, float scale, float* out,
+                                   float* lse_out, void* workspace, size_t ws_bytes, int32_t* status, void* stream)
+{
+    int rc = range_check(pool, q, H_q, page_table, max_pages, seq_lens, B, scale, out, status);
+    if (rc) return rc;
+    if (n_groups < 0 || n_groups > B) return ENTMAXKV_INVALID_ARG;
+    if (B == 0) return ENTMAXKV_OK;
+    if (n_groups > 0 && (!group_start || !prefix_lens)) return ENTMAXKV_INVALID_ARG;
+    const PrefixLayout lay = prefix_layout(B, H_q, pool->H_kv, pool->d);
+    if (!workspace || ws_bytes < lay.total || !aligned16(workspace)) return ENTMAXKV_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    PrefixArgs a{};
+    a.r = range_args(*pool, q, H_q, page_table, max_pages, seq_lens, B, scale, out, lse_out, ws, lay.range, status);
+    a.group_start = group_start;
+    a.prefix_lens = prefix_lens;
+    a.n_groups = pool->dtype == ENTMAXKV_BF16 ? n_groups : 0;
+    a.ps = pool->ps;
+    a.row_tile = kPrefixRows;
+    a.block_tok = 128;
+    a.C = lay.C;
+    a.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
+    a.gid = reinterpret_cast<int32_t*>(ws + lay.gid);
+    a.groups = reinterpret_cast<PrefixGroup*>(ws + lay.groups);
+    a.total = reinterpret_cast<long long*>(ws + lay.total_blocks);
+    a.span = reinterpret_cast<int2*>(ws + lay.span);
+    a.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+    a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml);
+    a.r.shared = a.shared;
+    CUtensorMap kmap, vmap;
+    if (pool->dtype == ENTMAXKV_BF16) {
+        if ((rc = make_pool_map(&kmap, *pool, pool->k_pool))) return rc;
+        if ((rc = make_pool_map(&vmap, *pool, pool->v_pool))) return rc;
+    }
+    return launch_prefix(*pool, a, lay.range.C, &kmap, &vmap, static_cast<cudaStream_t>(stream));
+}
+
 int entmaxkv_copy_pages(const entmaxkv_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
                         void* workspace, size_t ws_bytes, int32_t* status, void* stream)
 {
@@ -607,6 +678,7 @@ size_t entmaxkv_workspace_size(int32_t op, int32_t B, int32_t H_q, int32_t H_kv,
     if (B <= 0 || H_q <= 0 || H_kv <= 0 || max_pages <= 0 || ps <= 0 || d <= 0) return 0;
     if (op == ENTMAXKV_OP_SELECT) return 0;
     if (op == ENTMAXKV_OP_WINDOW_SOFTMAX) return range_layout(B, H_q, H_kv, d).total;
+    if (op == ENTMAXKV_OP_PREFIX_SOFTMAX) return prefix_layout(B, H_q, H_kv, d).total;
     if (is_sparse(op) && k_max <= 0) return 0;
     if (!is_sparse(op) && op != ENTMAXKV_OP_FULL_ENTMAX && op != ENTMAXKV_OP_FULL_SOFTMAX) return 0;
     return attn_layout(op, B, H_q, H_kv, max_pages, k_max, ps, d).total;

@@ -48,11 +48,11 @@ EKV_DEV void range_store(const RangeArgs& a, bool whole, long long slot, int b, 
 {
     float* dst;
     if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
         const size_t row = (size_t)b * a.H_q + (size_t)g * a.G + h;
         dst = a.out + row * D + d;
-        if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     } else {
         const size_t row = (size_t)slot * a.G + h;
         dst = a.part_o + row * D + d;
