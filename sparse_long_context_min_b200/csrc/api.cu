@@ -589,7 +589,7 @@ int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, in
     a.n_groups = pool->dtype == ENTMAXKV_BF16 ? n_groups : 0;
     a.ps = pool->ps;
     a.row_tile = kPrefixRows;
-    a.block_tok = 128;
+    a.block_tok = 64;
     a.C = lay.C;
     a.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
     a.gid = reinterpret_cast<int32_t*>(ws + lay.gid);

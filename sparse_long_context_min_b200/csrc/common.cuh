@@ -122,6 +122,17 @@ EKV_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns)
     }
 }
 
+// The same for waits whose end others wait for in turn: the timer, whose reading
+// takes longer than most such waits, comes in only after some of them have run out.
+EKV_DEV bool mbar_wait_chain(uint64_t* bar, uint32_t parity, uint64_t limit_ns)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+        if (mbar_try_wait_for(bar, parity, 100000u)) return true;
+    return mbar_wait(bar, parity, limit_ns);
+}
+
 // 2-D TMA tile load global -> shared, completion counted on `bar` in bytes.
 // x (innermost coordinate, elements) must be a multiple of 8 for bf16.
 EKV_DEV void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y)

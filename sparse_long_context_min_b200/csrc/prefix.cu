@@ -155,25 +155,36 @@ EKV_DEV void tc_dealloc(uint32_t addr, uint32_t cols)
 }
 EKV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 EKV_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-EKV_DEV void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (the loaded values pass through, so that their uses stay behind the wait)
+template <int N>
+EKV_DEV void tc_wait_ld(uint32_t* r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 EKV_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 EKV_DEV void tc_commit(uint64_t* bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
 }
-// D[tmem] (+)= A[smem] B[smem], or A[tmem] B[smem]; bf16 in, fp32 accumulators
-EKV_DEV void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+// Operand descriptors in shared memory, 128-byte swizzle: rows of 64 bf16,
+// groups of 8 rows 1024 bytes apart.  The low word holds the address and, for
+// an operand whose rows run along K (V), the distance of the next 64 columns;
+// the high word is the same for all.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+EKV_DEV uint32_t tc_desc(uint32_t addr, uint32_t lead)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+    return ((addr & 0x3FFFF) >> 4) | (((lead >> 4) & 0x3FFF) << 16);
 }
-EKV_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+// D[tmem] (+)= A[tmem] B[smem], bf16 in, fp32 accumulators; b is a descriptor's low word.
+EKV_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.u32 p, %4, 0;\n"
+                 " mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh) : "memory");
 }
 #define EKV_R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), \
                      "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
@@ -188,66 +199,131 @@ EKV_DEV void tc_ld32(uint32_t addr, uint32_t* r)
                  : EKV_R8(r, 0), EKV_R8(r, 8), EKV_R8(r, 16), EKV_R8(r, 24)
                  : "r"(addr));
 }
-EKV_DEV void tc_st32(uint32_t addr, const uint32_t* r)
+EKV_DEV void tc_ld16(uint32_t addr, uint32_t* r)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-                 ::EKV_W8(r, 0), EKV_W8(r, 8), EKV_W8(r, 16), EKV_W8(r, 24), "r"(addr) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : EKV_R8(r, 0), EKV_R8(r, 8)
+                 : "r"(addr));
+}
+EKV_DEV void tc_st16(uint32_t addr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+                 ::EKV_W8(r, 0), EKV_W8(r, 8), "r"(addr) : "memory");
+}
+EKV_DEV void tc_st8(uint32_t addr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 ::EKV_W8(r, 0), "r"(addr) : "memory");
 }
 
-// Shared-memory operand descriptors, 128-byte swizzle: rows of 64 bf16, groups
-// of 8 rows 1024 bytes apart.  `lead` is the distance of the next 64 columns
-// of an operand whose rows run along K (V), unused where they run along K only.
-EKV_DEV uint64_t tc_desc(uint32_t addr, uint32_t lead)
+// ---------------------------------------------------------------- pairs of floats
+EKV_DEV uint64_t pair(uint32_t x, uint32_t y)
 {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)((lead >> 4) & 0x3FFF) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+EKV_DEV uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
+EKV_DEV float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+EKV_DEV uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+EKV_DEV uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+// 2^x for scores below their row's maximum (plus 8): results under 2^-126 become zero
+EKV_DEV float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// integers in the order of the floats
+EKV_DEV int ordered_int(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+EKV_DEV float ordered_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+EKV_DEV uint32_t bf16x2(float2 v)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    return r;
 }
 
 // ---------------------------------------------------------------- bf16 cache
-// One persistent CTA an SM.  Blocks of 128 tokens; S has two buffers and O two
-// accumulators in tensor memory (4 x 128 columns): the two softmax warpgroups
-// take the blocks in turn, each with its own running maximum, sum and O, so
-// that neither waits for the other, and the products of one block run while
-// the other block's weights are made.
-//   warp 8  fills a ring of token blocks (K and V alternating) by TMA;
-//   warp 9  issues the products: S = (Q_hi + Q_lo) K^T from shared memory,
-//           O += (P_hi + P_lo) V with P read from tensor memory (it replaces S
-//           there);
-//   warps 0-3 / 4-7  one row a thread: maximum, weights, sum, P.
-// Query and weights enter as a bf16 high and low part (2^-17 of relative error
-// together), which doubles the products: at 128 rows 4 x 512 tensor cycles a
-// block stand against ~2700 cycles in which HBM delivers its 64 KB, so the
-// bytes still bound the time; more rows than a tile's 128 make the products
-// bound it.  O is rescaled only when the maximum grew by more than 2^8, which
-// keeps every weight in range and rescaling rare.
-constexpr int kPfxRows = 128, kPfxTok = 128;
-constexpr int kPfxThreads = 384;         // registers are dealt by warpgroup: two idle warps complete the third
+// One persistent CTA an SM walks its share of blocks of 64 tokens.  Tensor
+// memory (512 columns at 128 dims): two accumulators O, two score buffers S,
+// and Q.  Two sets of eight softmax warps take the blocks in turn, each set
+// with its own running maximum, sum and O, so that neither waits for the other
+// and the products of one block run while the other block's weights are made.
+//   warps 0-15   four a row quarter: set, and half of the block's tokens; one
+//                row a lane: maximum, weights, sum, P in place of S;
+//   warp 16      fills a ring of token blocks (K and V alternating) by TMA;
+//   warp 17      issues the products S = (Q_hi + Q_lo) K^T and
+//                O += (P_hi + P_lo) V, with Q and P read from tensor memory, so
+//                that shared memory feeds one operand only.
+// Query and weights enter as a bf16 high and low part (2^-18 of relative error
+// each), which doubles the products: at 128 rows 1024 tensor cycles a block
+// stand against ~1300 in which HBM delivers its 32 KB, so the bytes still
+// bound the time; more rows than a tile's 128 make the products bound it.  O is
+// rescaled only when the maximum grew by more than 2^8, which keeps every
+// weight in range and rescaling rare.
+constexpr int kPfxRows = 128, kPfxTok = 64;
+constexpr int kPfxSoft = 16;             // softmax warps
+constexpr int kPfxThreads = (kPfxSoft + 2) * 32;
 constexpr float kPfxLazy = 8.f;
 
 template <int D>
-constexpr int pfx_slots() { return D == 128 ? 5 : 8; }
+constexpr int pfx_slots() { return D == 128 ? 13 : 24; }
 
-// 384 x 168 registers at launch: 128 x 40 for the producer and product warps
-// leave 256 x 232 for the softmax, which holds a row's 128 scores.
-EKV_DEV void regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
-EKV_DEV void regs_many() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
+// A value that all lanes of the warp hold, told to the compiler: the tensor
+// instructions take their operands from the warp's uniform registers, and one
+// that has to be moved there first costs the issuing warp more than the product.
+template <typename T>
+EKV_DEV T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+EKV_DEV bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
 
-EKV_DEV void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+EKV_DEV void bar_softmax() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// the two warps that share rows' scores
+EKV_DEV void bar_halves(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id + 2) : "memory"); }
 
 // Bounded wait of a warp, the same answer in all its lanes; a wait that ran out
 // marks the CTA dead, after which every role runs to its end without waiting or
 // issuing.
-EKV_DEV bool pfx_wait(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status)
+__device__ __noinline__ bool pfx_wait_long(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status)
 {
     bool ok = !*dead;
-    if (ok && !mbar_wait(bar, parity, kWaitLimitNs)) {
+    if (ok && !mbar_wait_chain(bar, parity, kWaitLimitNs)) {
         ok = false;
         *dead = 1;
         report(status, ENTMAXKV_TIMEOUT);
     }
     return __all_sync(0xffffffffu, ok);
+}
+EKV_DEV bool pfx_wait(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* status)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return pfx_wait_long(bar, parity, dead, status);
 }
 
 template <int D, int PS>
@@ -255,22 +331,23 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                                                                      const __grid_constant__ CUtensorMap vmap,
                                                                      const PrefixArgs a)
 {
-    pdl_enter();
     constexpr int SLOTS = pfx_slots<D>();
-    constexpr int HALF = kPfxTok * 128;                // bytes of 64 columns of a block or of Q
+    constexpr int HALF = kPfxTok * 128;                // bytes of 64 columns of a block
     constexpr int TILE = HALF * (D / 64);
     constexpr int PPB = kPfxTok / PS;                  // pages a block
+    constexpr int QD = D / 4;                          // dims of a row that one thread stages
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_align<1024>(smem_raw);
-    uint8_t* qs = smem;                                // Q high part, then low part
-    uint8_t* ring = smem + 2 * TILE;
+    uint8_t* ring = smem_align<1024>(smem_raw);
     __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], q_full, o_full;
     __shared__ uint32_t tmem_slot;
     __shared__ PrefixWalk start;
+    __shared__ int top_of[2][kPfxRows];                // [set][row] largest score so far, as an ordered integer
+    __shared__ float2 ml[4][kPfxRows];
     __shared__ volatile int dead;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     int32_t* status = a.r.status;
 
+    // nothing here touches global memory: it runs under the end of the kernel before
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&full[i], 1);
@@ -278,286 +355,315 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
         }
-        mbar_init(&q_full, 8);
+        mbar_init(&q_full, kPfxSoft);
         mbar_init(&o_full, 1);
         fence_mbar_init();
         dead = 0;
-        start = prefix_start(a, blockIdx.x);
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
     }
-    __syncthreads();
-    PrefixWalk w = start;
-    if (w.left <= 0) return;
-    if (warp == 9) tc_alloc(&tmem_slot, 512);
+    if (warp == kPfxSoft + 1) tc_alloc(&tmem_slot, 512);
+    pdl_enter();
+    if (tid == 0) start = prefix_start(a, blockIdx.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    const uint32_t O[2] = {tmem, tmem + 128}, S[2] = {tmem + 256, tmem + 384};
+    PrefixWalk w = start;
+    const uint32_t tmem = uniform(tmem_slot);
+    const uint32_t O[2] = {tmem, tmem + 128}, S[2] = {tmem + 256, tmem + 320}, Q = tmem + 384;
 
-    // setmaxnreg stands inside its role: code that both roles reach would get the smaller share
-    if (warp < 8) {
+    if (warp < kPfxSoft) {
         // ---------------------------------------------------- softmax
-        regs_many();
-        const int wg = warp >> 2, quad = warp & 3;
+        const int set = warp >> 3, half = (warp >> 2) & 1, quarter = warp >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t at = S[set] + lanes + half * 32, acc = O[set] + lanes + half * (D / 2);
+        const int lg = __ffs(a.r.G) - 1;
+        float4 qv[QD / 4];                             // this thread's part of its row's query
+        auto load_q = [&] {
+            const PrefixGroup& G = a.groups[w.j];
+            const int r = w.t * kPfxRows + row;
+            const float* q = a.r.q + ((size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1))) * D +
+                             quarter * QD;
+#pragma unroll
+            for (int e = 0; e < QD / 4; ++e)
+                qv[e] = r < G.rows ? reinterpret_cast<const float4*>(q)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        auto stage_q = [&] {
+            uint32_t hi[QD / 2], lo[QD / 2];
+            const float* v = reinterpret_cast<const float*>(qv);
+#pragma unroll
+            for (int e = 0; e < QD / 2; ++e) {
+                const float2 x = make_float2(v[2 * e] * a.r.xscale, v[2 * e + 1] * a.r.xscale);
+                hi[e] = bf16x2(x);
+                lo[e] = bf16x2(make_float2(x.x - __uint_as_float(hi[e] << 16), x.y - __uint_as_float(hi[e] & 0xffff0000u)));
+            }
+            const uint32_t dst = Q + lanes + quarter * (QD / 2);
+#pragma unroll
+            for (int e = 0; e < QD / 2; e += 8) {
+                tc_st8(dst + e, hi + e);
+                tc_st8(dst + D / 2 + e, lo + e);
+            }
+            if (half == 0) top_of[set][row] = ordered_int(-INFINITY);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+        };
         int seg = 0, s_n = 0;
+        if (w.left > 0) {
+            load_q();
+            stage_q();
+            bar_softmax();
+        }
         while (w.left > 0) {
-            const PrefixGroup G = a.groups[w.j];
+            const PrefixGroup& G = a.groups[w.j];
             const int n = (int)min((long long)(G.blocks - w.k), w.left);
             const int rows = min(kPfxRows, G.rows - w.t * kPfxRows);
+            // tokens from this warp's first column of the first block to the end of the shared pages
+            const int ahead = (int)min((long long)G.pages * PS - (long long)w.k * kPfxTok - half * 32, 0x7fffffffll);
+            const long long part_row = prefix_part_row(a, G, w.g, w.t, blockIdx.x);
             if (tid == 0) prefix_note_span(a, w, G, blockIdx.x);
-            // Q, scaled and split, a warp a row
-            for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 4) {
-                float v[4][D / 32];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int rr = w.t * kPfxRows + r0 + r;
-                    const bool in = r0 + r < rows;
-                    const size_t at = ((size_t)(G.lo + rr / a.r.G) * a.r.H_q + (size_t)w.g * a.r.G + rr % a.r.G) * D;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e)
-                        v[r][e] = in ? a.r.q[at + (e / 2) * 64 + 2 * lane + (e & 1)] * a.r.xscale : 0.f;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const int rr = r0 + r;
-                        uint32_t h0, l0, h1, l1;
-                        split_bf16(v[r][2 * h], h0, l0);
-                        split_bf16(v[r][2 * h + 1], h1, l1);
-                        const uint32_t o = h * HALF + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4;
-                        *reinterpret_cast<uint32_t*>(qs + o) = pack2(h0, h1);
-                        *reinterpret_cast<uint32_t*>(qs + TILE + o) = pack2(l0, l1);
-                    }
-            }
-            fence_proxy_async();
-            tc_fence_before();                         // the last unit's reads of O
-            bar_softmax();
-            if (lane == 0) mbar_arrive(&q_full);
 
             float m = -INFINITY, l = 0.f;
-            for (int i = wg; i < n; i += 2) {
-                const bool ok = pfx_wait(&s_full[wg], s_n++ & 1, &dead, status);
+            for (int i = set; i < n; i += 2, ++s_n) {
+                const bool ok = pfx_wait(&s_full[set], s_n & 1, &dead, status);
                 tc_fence_after();
                 if (ok && quad * 32 < rows) {
-                    uint32_t s[128];
+                    uint32_t s[32];
+                    tc_ld32(at, s);
+                    tc_wait_ld<32>(s);
+                    const int valid = ahead - i * kPfxTok;
+                    if (valid < 32)                    // columns past the shared pages
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tc_ld32(S[wg] + lanes + c * 32, s + c * 32);
-                    tc_wait_ld();
-                    const int valid = min(kPfxTok, (int)min((long long)G.pages * PS - (long long)(w.k + i) * kPfxTok,
-                                                            (long long)kPfxTok));
-                    if (valid < kPfxTok)
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c >= valid) s[c] = 0xff800000u;
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= valid) s[e] = 0xff800000u;
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+                    // both halves raise the row's maximum (the next block's scores only come when both have
+                    // given up this block's weights, so nobody raises it before it has been read)
+                    atomicMax(&top_of[set][row], ordered_int(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]))));
+                    bar_halves(set * 4 + quad);
+                    const float top = ordered_float(*(volatile int*)&top_of[set][row]);
                     const bool grow = top > m + kPfxLazy || m == -INFINITY;
-                    const float mnew = grow ? fmaxf(top, m) : m;
+                    const float mnew = grow ? top : m;
                     if (i >= 2 && __any_sync(0xffffffffu, grow)) {
                         // the products into this O before this block's scores have finished with them
-                        const float f = m == -INFINITY ? 0.f : exp2f(m - mnew);
+                        const float f = m == -INFINITY ? 0.f : ex2(m - mnew);
                         l *= f;
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tc_ld32(O[wg] + lanes + c, o);
-                            tc_wait_ld();
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 16) {
+                            uint32_t o[16];
+                            tc_ld16(acc + c, o);
+                            tc_wait_ld<16>(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st32(O[wg] + lanes + c, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st16(acc + c, o);
                         }
                     }
                     m = mnew;
                     const float mu = m == -INFINITY ? 0.f : m;
-                    float sum[2] = {0.f, 0.f};
+                    const uint64_t down = pair(-mu, -mu), minus = pair(-1.f, -1.f);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 128; c += 64) {
-                        uint32_t hi[32], lo[32];
+                    for (int c = 0; c < 32; c += 16) {
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = exp2f(__uint_as_float(s[c + 2 * e]) - mu);
-                            const float p1 = exp2f(__uint_as_float(s[c + 2 * e + 1]) - mu);
-                            sum[0] += p0;
-                            sum[1] += p1;
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi[e]) : "f"(p1), "f"(p0));
-                            const float r0 = p0 - __uint_as_float(hi[e] << 16);
-                            const float r1 = p1 - __uint_as_float(hi[e] & 0xffff0000u);
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(r1), "f"(r0));
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 y = unpair(add2(pair(s[c + 2 * e], s[c + 2 * e + 1]), down));
+                            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                            const uint64_t pp = pair(p.x, p.y);
+                            sum[e & 1] = add2(sum[e & 1], pp);
+                            hi[e] = bf16x2(p);
+                            lo[e] = bf16x2(unpair(fma2(pair(hi[e] << 16, hi[e] & 0xffff0000u), minus, pp)));
                         }
-                        tc_st32(S[wg] + lanes + c / 2, hi);
-                        tc_st32(S[wg] + lanes + 64 + c / 2, lo);
+                        // weights in place of their scores: of 16 tokens 8 words of high, 8 of low parts
+                        tc_st8(at + c, hi);
+                        tc_st8(at + c + 8, lo);
                     }
-                    l += sum[0] + sum[1];
+                    const float2 t = unpair(add2(sum[0], sum[1]));
+                    l += t.x + t.y;
                     tc_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[wg]);
+                if (lane == 0) mbar_arrive(&p_full[set]);
             }
-            // join the two accumulators: warpgroup x takes columns [x D/2, (x + 1) D/2) of every row
+            // the next unit's query goes out before this unit's results: its first products run meanwhile
+            prefix_advance(a, w, n);
+            if (w.left > 0) load_q();
             const bool ok = pfx_wait(&o_full, seg & 1, &dead, status);
             tc_fence_after();
-            float* ml = reinterpret_cast<float*>(qs);  // Q is not read any more
-            ml[(wg * kPfxRows + row) * 2] = m;
-            ml[(wg * kPfxRows + row) * 2 + 1] = l;
-            bar_softmax();
+            ml[quarter][row] = make_float2(m, l);
+            bar_softmax();                             // also: nobody reads this unit's maxima any more
+            if (w.left > 0) stage_q();
+            // join the two accumulators: a warp takes D/4 columns of its rows
             if (ok && quad * 32 < rows) {
-                const float m0 = ml[row * 2], m1 = ml[(kPfxRows + row) * 2];
+                const float m0 = ml[0][row].x, m1 = ml[2][row].x;
                 const float M = fmaxf(m0, m1);
-                const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-                const float L = ml[row * 2 + 1] * f0 + ml[(kPfxRows + row) * 2 + 1] * f1;
-                const long long pr = prefix_part_row(a, G, w.g, w.t, blockIdx.x) + row;
+                const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+                // partials lie [D / 4][rows] float4: the lanes of a warp store 512 consecutive bytes
+                float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * D) + row;
 #pragma unroll
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t x[32], y[32];
-                    tc_ld32(O[0] + lanes + wg * (D / 2) + c, x);
-                    if (n > 1) tc_ld32(O[1] + lanes + wg * (D / 2) + c, y);
-                    tc_wait_ld();
-                    if (row < rows) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + wg * (D / 2) + c);
+                for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+                    uint32_t x[16], y[16] = {};
+                    tc_ld16(O[0] + lanes + c, x);
+                    if (n > 1) tc_ld16(O[1] + lanes + c, y);
+                    tc_wait_ld<16>(x);
+                    tc_wait_ld<16>(y);
+                    if (row < rows)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 16; e += 4) {
                             float o[4];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                o[q] = __uint_as_float(x[4 * e + q]) * f0;
-                                if (n > 1) o[q] = fmaf(__uint_as_float(y[4 * e + q]), f1, o[q]);
+                                o[q] = __uint_as_float(x[e + q]) * f0;
+                                if (n > 1) o[q] = fmaf(__uint_as_float(y[e + q]), f1, o[q]);
                             }
-                            dst[e] = make_float4(o[0], o[1], o[2], o[3]);
+                            dst[(c + e) / 4 * rows] = make_float4(o[0], o[1], o[2], o[3]);
                         }
-                    }
                 }
-                if (row < rows && wg == 0) {
-                    a.part_ml[pr * 2] = M;
-                    a.part_ml[pr * 2 + 1] = L;
-                }
+                if (row < rows && quarter == 0)
+                    reinterpret_cast<float2*>(a.part_ml)[part_row + row] =
+                        make_float2(M, (ml[0][row].y + ml[1][row].y) * f0 + (ml[2][row].y + ml[3][row].y) * f1);
             }
-            bar_softmax();                             // the maxima have been read: Q may come again
+            tc_fence_before();
+            bar_softmax();                             // O and ml may come again
             ++seg;
-            prefix_advance(a, w, n);
         }
-    } else {
-        regs_few();
-        if (warp == 8) {
-            // ---------------------------------------------------- producer
-            if (lane == 0) {
-                prefetch_tmap(&kmap);
-                prefetch_tmap(&vmap);
+    } else if (warp == kPfxSoft) {
+        // ---------------------------------------------------- producer
+        int it = 0;                                    // ring slots filled so far
+        auto load = [&](const CUtensorMap* map, int g, int ph) {
+            // lanes < PPB hold the block's physical pages (-1: none)
+            const int slot = it % SLOTS;
+            const bool go = it < SLOTS || pfx_wait(&empty[slot], (uint32_t)((it / SLOTS - 1) & 1), &dead, status);
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < PPB && ph >= 0);
+            if (go) {
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(good) * PS * D * 2);
+                __syncwarp();
+                if (lane < PPB && ph >= 0)
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_2d(ring + slot * TILE + h * HALF + lane * PS * 128, map, &full[slot], h * 64,
+                                    (ph * a.r.H_kv + g) * PS);
+                ++it;
             }
-            int it = 0;                                    // ring slots filled so far
-            auto load = [&](const CUtensorMap* map, const PrefixGroup& G, int g, int blk, int ph) {
-                // lanes < PPB hold the block's physical pages (-1: none)
-                const int slot = it % SLOTS;
-                const bool go = it < SLOTS || pfx_wait(&empty[slot], (uint32_t)((it / SLOTS - 1) & 1), &dead, status);
-                const uint32_t good = __ballot_sync(0xffffffffu, lane < PPB && ph >= 0);
-                if (go) {
-                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(good) * PS * D * 2);
-                    __syncwarp();
-                    if (lane < PPB && ph >= 0)
-    #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_2d(ring + slot * TILE + h * HALF + lane * PS * 128, map, &full[slot], h * 64,
-                                        (ph * a.r.H_kv + g) * PS);
-                    ++it;
-                }
-                return go;
-            };
-            bool go = true;
-            while (w.left > 0 && go) {
-                const PrefixGroup G = a.groups[w.j];
-                const int n = (int)min((long long)(G.blocks - w.k), w.left);
+            return go;
+        };
+        bool go = true;
+        while (w.left > 0 && go) {
+            const PrefixGroup& G = a.groups[w.j];
+            const int n = (int)min((long long)(G.blocks - w.k), w.left), g = w.g;
+            const int32_t* pages = a.r.page_table + (size_t)G.first * a.r.max_pages;
+            // 32 blocks' pages at a time would hide their loads; one block ahead does, behind the ring
+            auto page = [&](int blk) {
+                if (lane >= PPB) return -1;
                 // pages past the shared ones repeat the block's first page: their scores are masked, and
                 // the weight of zero they get must meet a value that some row uses anyway
-                auto page = [&](int blk) {
-                    if (lane >= PPB) return -1;
-                    int p = blk * PPB + lane;
-                    if (p >= G.pages) p = blk * PPB;
-                    const int ph = a.r.page_table[(size_t)G.first * a.r.max_pages + p];
-                    if (ph < 0 || ph >= a.r.num_phys) {
-                        report(status, ENTMAXKV_DEVICE_BOUNDS);
-                        return -1;
-                    }
-                    return ph;
-                };
-                int ph = page(w.k), prev = -1;
-                for (int i = 0; i <= n && go; ++i) {
-                    const int next = i + 1 < n ? page(w.k + i + 1) : -1;
-                    if (i < n) go = load(&kmap, G, w.g, w.k + i, ph);
-                    if (i > 0 && go) go = load(&vmap, G, w.g, w.k + i - 1, prev);
-                    prev = ph;
-                    ph = next;
+                int p = blk * PPB + lane;
+                if (p >= G.pages) p = blk * PPB;
+                const int ph = pages[p];
+                if (ph < 0 || ph >= a.r.num_phys) {
+                    report(status, ENTMAXKV_DEVICE_BOUNDS);
+                    return -1;
                 }
-                prefix_advance(a, w, n);
+                return ph;
+            };
+            int ph = page(w.k), prev = -1;
+            for (int i = 0; i <= n && go; ++i) {
+                const int next = i + 1 < n ? page(w.k + i + 1) : -1;
+                if (i < n) go = load(&kmap, g, ph);
+                if (i > 0 && go) go = load(&vmap, g, prev);
+                prev = ph;
+                ph = next;
             }
-            if (!go && lane == 0)
-                for (int i = max(0, it - SLOTS); i < it; ++i)
-                    mbar_wait(&full[i % SLOTS], (uint32_t)((i / SLOTS) & 1), kWaitLimitNs);
-        } else if (warp == 9) {
-            // ---------------------------------------------------- products
-            constexpr uint32_t ID = (1u << 4) | (1u << 7) | (1u << 10) | ((kPfxRows / 16) << 24);
-            constexpr uint32_t ID_QK = ID | ((kPfxTok / 8) << 17), ID_PV = ID | (1u << 16) | ((D / 8) << 17);
-            const uint32_t q_addr = smem_addr(qs), r_addr = smem_addr(ring);
-            int it = 0, seg = 0;
-            int s_it[2] = {0, 0};                          // blocks given to each warpgroup
-            while (w.left > 0) {
-                const PrefixGroup G = a.groups[w.j];
-                const int n = (int)min((long long)(G.blocks - w.k), w.left);
-                bool ok = pfx_wait(&q_full, seg & 1, &dead, status);
-                tc_fence_after();
-                auto scores = [&](int i) {
-                    const int slot = it % SLOTS;
-                    ok = pfx_wait(&full[slot], (uint32_t)((it / SLOTS) & 1), &dead, status) && ok;
-                    ++it;
-                    if (!ok || lane != 0) return;
-                    const uint32_t kb = r_addr + slot * TILE;
-    #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-    #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t o = (k / 4) * HALF + (k % 4) * 32;
-                            tc_mma_ss(S[i & 1], tc_desc(q_addr + part * TILE + o, 16), tc_desc(kb + o, 16), ID_QK,
-                                      part + k > 0);
-                        }
-                    tc_commit(&empty[slot]);
-                    tc_commit(&s_full[i & 1]);
-                };
-                auto values = [&](int i) {
-                    const int slot = it % SLOTS, x = i & 1;
-                    ok = pfx_wait(&full[slot], (uint32_t)((it / SLOTS) & 1), &dead, status) && ok;
-                    ++it;
-                    ok = pfx_wait(&p_full[x], s_it[x]++ & 1, &dead, status) && ok;
-                    tc_fence_after();
-                    if (!ok || lane != 0) return;
-                    const uint32_t vb = r_addr + slot * TILE;
-    #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-    #pragma unroll
-                        for (int k = 0; k < kPfxTok / 16; ++k)
-                            tc_mma_ts(O[x], S[x] + part * 64 + k * 8, tc_desc(vb + k * 2048, HALF), ID_PV,
-                                      i > 1 || part + k > 0);
-                    tc_commit(&empty[slot]);
-                };
-                for (int i = 0; i <= n; ++i) {
-                    if (i < n) scores(i);
-                    if (i > 0) values(i - 1);
-                }
-                if (lane == 0 && ok) tc_commit(&o_full);
-                __syncwarp();
-                ++seg;
-                prefix_advance(a, w, n);
+            prefix_advance(a, w, n);
+        }
+        if (!go && lane == 0)
+            for (int i = max(0, it - SLOTS); i < it; ++i)
+                mbar_wait(&full[i % SLOTS], (uint32_t)((i / SLOTS) & 1), kWaitLimitNs);
+    } else {
+        // ---------------------------------------------------- products
+        constexpr uint32_t ID = (1u << 4) | (1u << 7) | (1u << 10) | ((kPfxRows / 16) << 24);
+        constexpr uint32_t ID_QK = ID | ((kPfxTok / 8) << 17), ID_PV = ID | (1u << 16) | ((D / 8) << 17);
+        const uint32_t ring0 = uniform(smem_addr(ring));
+        int slot = 0, seg = 0;
+        uint32_t filled = 0, given[2] = {0, 0};        // parities: ring slots, blocks given to each set
+        auto next_slot = [&] {
+            if (++slot == SLOTS) {
+                slot = 0;
+                filled ^= 1;
             }
+        };
+        auto scores = [&](int x) {
+            if (!pfx_wait(&full[slot], filled, &dead, status)) return;
+            const uint32_t kd = tc_desc(ring0 + slot * TILE, 16);
+            if (elect_one()) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ts(S[x], Q + part * (D / 2) + k * 8, kd + (((k / 4) * HALF + (k % 4) * 32) >> 4), ID_QK,
+                                  part + k > 0);
+                tc_commit(&empty[slot]);
+                tc_commit(&s_full[x]);
+            }
+            __syncwarp();
+            next_slot();
+        };
+        auto values = [&](int x, bool first) {
+            if (!pfx_wait(&full[slot], filled, &dead, status)) return;
+            const bool ok = pfx_wait(&p_full[x], given[x], &dead, status);
+            given[x] ^= 1;
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t vd = tc_desc(ring0 + slot * TILE, HALF);
+            if (elect_one()) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < kPfxTok / 16; ++k)
+                        tc_mma_ts(O[x], S[x] + k * 16 + part * 8, vd + ((k * 2048) >> 4), ID_PV,
+                                  part + k > 0 || !first);
+                tc_commit(&empty[slot]);
+            }
+            __syncwarp();
+            next_slot();
+        };
+        while (uniform(w.left > 0)) {
+            const int n = uniform((int)min((long long)(a.groups[w.j].blocks - w.k), w.left));
+            pfx_wait(&q_full, seg & 1, &dead, status);
+            tc_fence_after();
+            // S0, then S1 V0, S0 V1, ...: each set's scores are made while the other's weights are
+            scores(0);
+            int i = 1;
+            for (; i + 1 < n; i += 2) {
+                scores(1);
+                values(0, i == 1);
+                scores(0);
+                values(1, i == 1);
+            }
+            if (i < n) {
+                scores(1);
+                values(0, i == 1);
+                values(1, i == 1);
+            } else {
+                values(0, i == 1);
+            }
+            if (__all_sync(0xffffffffu, !dead) && elect_one()) tc_commit(&o_full);
+            __syncwarp();
+            ++seg;
+            prefix_advance(a, w, n);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tc_dealloc(tmem, 512);
+    if (warp == kPfxSoft + 1) tc_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- merge
@@ -571,6 +677,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a)
     const SeqSpan sp = seq_span(r, b, a.ps, false);
     const int j = a.gid[b];
     int n_own = 0, n_pfx = 0;
+    int rows = 0, row0 = 0;                            // rows of its tile, and its first among them
     long long own0 = 0, pfx0 = 0;
     if (sp.pages() > 0) {
         const int2 s = r.span[u];
@@ -582,22 +689,26 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a)
         const int row = (b - G.lo) * r.G, t = row / a.row_tile;
         const int2 s = a.span[prefix_unit(G, g, t)];
         n_pfx = s.y - s.x + 1;
-        pfx0 = prefix_part_row(a, G, g, t, s.x) + row % a.row_tile;
+        pfx0 = prefix_part_row(a, G, g, t, s.x);
+        row0 = row % a.row_tile;
+        rows = min(a.row_tile, G.rows - t * a.row_tile);
     }
     for (int i = threadIdx.x; i < r.G * D / 4; i += blockDim.x) {
-        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        const int h = i & (r.G - 1), d4 = i / r.G;     // a tile's partials lie [D / 4][rows] float4
         float M = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float* po, const float* pml, long long row, long long step, int n) {
+        // n partials, `step` rows apart; a row's maximum and sum lie at ml + its row
+        auto add = [&](const float* po, const float* pml, long long step, int n) {
+            const float4* p4 = reinterpret_cast<const float4*>(po);
+            const float2* p2 = reinterpret_cast<const float2*>(pml);
             for (int s0 = 0; s0 < n; s0 += 8) {
                 float4 t[8];
                 float2 ml[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (s0 + k < n) {
-                        const long long at = row + (s0 + k) * step;
-                        t[k] = *reinterpret_cast<const float4*>(po + at * D + d);
-                        ml[k] = *reinterpret_cast<const float2*>(pml + at * 2);
+                        t[k] = p4[(s0 + k) * step * (D / 4)];
+                        ml[k] = p2[(s0 + k) * step];
                     }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -613,16 +724,17 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a)
                     }
             }
         };
-        add(a.part_o, a.part_ml, pfx0 + h, a.row_tile, n_pfx);
-        add(r.part_o, r.part_ml, own0 + h, r.G, n_own);
+        add(a.part_o + pfx0 * D + ((long long)d4 * rows + row0 + h) * 4, a.part_ml + (pfx0 + row0 + h) * 2, a.row_tile,
+            n_pfx);
+        add(r.part_o + (own0 + h) * D + d4 * 4, r.part_ml + (own0 + h) * 2, r.G, n_own);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t row = (size_t)b * r.H_q + (size_t)g * r.G + h;
-        float* dst = r.out + row * D + d;
+        float* dst = r.out + row * D + d4 * 4;
         dst[0] = o.x * inv;
         dst[1] = o.y * inv;
         dst[2] = o.z * inv;
         dst[3] = o.w * inv;
-        if (d == 0 && r.lse) r.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        if (d4 == 0 && r.lse) r.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
     }
 }
 
@@ -631,7 +743,7 @@ template <int D, int PS>
 static int launch_prefix_bf16(const PrefixArgs& a, const CUtensorMap* kmap, const CUtensorMap* vmap,
                               cudaStream_t stream)
 {
-    const int smem = (2 + pfx_slots<D>()) * kPfxTok * D * 2 + 1024;
+    const int smem = pfx_slots<D>() * kPfxTok * D * 2 + 1024;
     if (ensure_smem((const void*)prefix_bf16_kernel<D, PS>, smem)) return ENTMAXKV_CUDA_ERROR;
     return launch_pdl(prefix_bf16_kernel<D, PS>, dim3(a.C), dim3(kPfxThreads), smem, stream, *kmap, *vmap, a) ==
                    cudaSuccess
