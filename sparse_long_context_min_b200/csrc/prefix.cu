@@ -27,19 +27,21 @@ constexpr int kPrefixPlanThreads = 512;
 __global__ void __launch_bounds__(kPrefixPlanThreads) prefix_plan_kernel(const PrefixArgs a)
 {
     pdl_enter();
-    __shared__ long long wsum[3][kPrefixPlanThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = kPrefixPlanThreads / 32;
+    constexpr int N = kPrefixPlanThreads, CHUNK = N - 1;   // groups at a time: their bounds are one more
+    __shared__ int bound[N], pages_of[N], first_of[N], wmax[N / 32];
+    __shared__ long long wsum[2][N / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = N / 32;
     const int B = a.r.B, G = a.r.G;
-    for (int b = tid; b < B; b += kPrefixPlanThreads) {
+    for (int b = tid; b < B; b += N) {
         a.shared[b] = 0;
         a.gid[b] = -1;
     }
-    __shared__ int wmax[kPrefixPlanThreads / 32], end;
     int top = 0;                                       // largest bound so far
-    for (int j0 = 0; j0 <= a.n_groups && a.n_groups > 0; j0 += kPrefixPlanThreads) {
-        const int j = j0 + tid;
+    long long rows0 = 0, blocks0 = 0;
+    for (int j0 = 0; j0 < a.n_groups; j0 += CHUNK) {
+        const int cnt = min(CHUNK, a.n_groups - j0), j = j0 + tid;
         int v = 0;
-        if (j <= a.n_groups) {
+        if (tid <= cnt) {
             const int s = a.group_start[j];
             v = min(max(s, 0), B);
             if (v != s) report(a.r.status, ENTMAXKV_DEVICE_BOUNDS);
@@ -50,95 +52,80 @@ __global__ void __launch_bounds__(kPrefixPlanThreads) prefix_plan_kernel(const P
             const int t = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc = max(inc, t);
         }
-        __syncthreads();
         if (lane == 31) wmax[warp] = inc;
         __syncthreads();
-        int next = top;
-        for (int i = 0; i < nw; ++i) {
-            if (i < warp) top = max(top, wmax[i]);
-            next = max(next, wmax[i]);
-        }
+        for (int i = 0; i < warp; ++i) top = max(top, wmax[i]);
         inc = max(inc, top);
-        if (j <= a.n_groups && inc != v) report(a.r.status, ENTMAXKV_DEVICE_BOUNDS);
-        if (j < a.n_groups) a.groups[j].lo = inc;
-        if (j == a.n_groups) end = inc;
-        top = next;
-    }
-    __syncthreads();
-    for (int j = warp; j < a.n_groups; j += nw) {
-        const int lo = a.groups[j].lo, hi = j + 1 < a.n_groups ? a.groups[j + 1].lo : end;
-        int shortest = INT32_MAX, some = 0, first = INT32_MAX;
-        for (int b = lo + lane; b < hi; b += 32) {
-            const int L = a.r.seq_lens[b];
-            if (L > 0) {
-                shortest = min(shortest, L);
-                first = min(first, b);
-                ++some;
+        if (tid <= cnt && inc != v) report(a.r.status, ENTMAXKV_DEVICE_BOUNDS);
+        bound[tid] = inc;
+        __syncthreads();
+        for (int i = warp; i < cnt; i += nw) {
+            const int lo = bound[i], hi = bound[i + 1];
+            int shortest = INT32_MAX, some = 0, first = INT32_MAX;
+            for (int b = lo + lane; b < hi; b += 32) {
+                const int L = a.r.seq_lens[b];
+                if (L > 0) {
+                    shortest = min(shortest, L);
+                    first = min(first, b);
+                    ++some;
+                }
+            }
+            shortest = __reduce_min_sync(0xffffffffu, shortest);
+            some = __reduce_add_sync(0xffffffffu, some);
+            first = __reduce_min_sync(0xffffffffu, first);
+            const int pages = some > 1 ? min(min(max(a.prefix_lens[j0 + i], 0), shortest) / a.ps, a.r.max_pages) : 0;
+            for (int b = lo + lane; b < hi; b += 32) {
+                a.shared[b] = pages;
+                a.gid[b] = j0 + i;
+            }
+            if (lane == 0) {
+                pages_of[i] = pages;
+                first_of[i] = first;
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            shortest = min(shortest, __shfl_xor_sync(0xffffffffu, shortest, o));
-            some += __shfl_xor_sync(0xffffffffu, some, o);
-            first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-        }
-        int pages = some > 1 ? min(max(a.prefix_lens[j], 0), shortest) / a.ps : 0;
-        pages = min(pages, a.r.max_pages);
-        for (int b = lo + lane; b < hi; b += 32) {
-            a.shared[b] = pages;
-            a.gid[b] = j;
-        }
-        if (lane == 0) {
-            PrefixGroup& g = a.groups[j];
-            g.n = hi - lo;
-            g.first = first;
-            g.pages = pages;
-            g.rows = pages ? g.n * G : 0;
+        __syncthreads();
+        // offsets of the groups' rows and blocks
+        PrefixGroup g{};
+        long long x[2] = {0, 0}, sum[2];
+        if (tid < cnt) {
+            g.lo = bound[tid];
+            g.n = bound[tid + 1] - g.lo;
+            g.first = first_of[tid];
+            g.pages = pages_of[tid];
+            g.rows = g.pages ? g.n * G : 0;
             g.tiles = (g.rows + a.row_tile - 1) / a.row_tile;
-            g.blocks = (int)(((long long)pages * a.ps + a.block_tok - 1) / a.block_tok);
-        }
-    }
-    __syncthreads();
-    // offsets of the groups' units, rows and blocks
-    long long units = 0, rows = 0, blocks = 0;
-    for (int j0 = 0; j0 < a.n_groups; j0 += kPrefixPlanThreads) {
-        const int j = j0 + tid;
-        long long v[3] = {0, 0, 0}, inc[3];
-        if (j < a.n_groups) {
-            const PrefixGroup& g = a.groups[j];
-            v[0] = (long long)a.r.H_kv * g.tiles;
-            v[1] = (long long)a.r.H_kv * g.rows;
-            v[2] = v[0] * g.blocks;
+            g.blocks = (int)(((long long)g.pages * a.ps + a.block_tok - 1) / a.block_tok);
+            x[0] = (long long)a.r.H_kv * g.rows;
+            x[1] = (long long)a.r.H_kv * g.tiles * prefix_len(g);
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            inc[x] = v[x];
+        for (int i = 0; i < 2; ++i) {
+            sum[i] = x[i];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, inc[x], o);
-                if (lane >= o) inc[x] += t;
+                const long long t = __shfl_up_sync(0xffffffffu, sum[i], o);
+                if (lane >= o) sum[i] += t;
             }
+            if (lane == 31) wsum[i][warp] = sum[i];
         }
         __syncthreads();
-        if (lane == 31)
-            for (int x = 0; x < 3; ++x) wsum[x][warp] = inc[x];
-        __syncthreads();
-        long long off[3] = {units, rows, blocks};
+        g.row0 = rows0 + sum[0] - x[0];
+        g.block0 = blocks0 + sum[1] - x[1];
         for (int i = 0; i < nw; ++i) {
-            units += wsum[0][i];
-            rows += wsum[1][i];
-            blocks += wsum[2][i];
-            if (i < warp)
-                for (int x = 0; x < 3; ++x) off[x] += wsum[x][i];
+            if (i < warp) {
+                g.row0 += wsum[0][i];
+                g.block0 += wsum[1][i];
+            }
+            rows0 += wsum[0][i];
+            blocks0 += wsum[1][i];
         }
-        if (j < a.n_groups) {
-            PrefixGroup& g = a.groups[j];
-            g.unit0 = (int)(off[0] + inc[0] - v[0]);
-            g.row0 = off[1] + inc[1] - v[1];
-            g.block0 = off[2] + inc[2] - v[2];
-        }
+        if (tid < cnt) a.groups[j] = g;
+        top = bound[cnt];
+        __syncthreads();
     }
-    if (tid == 0) *a.total = blocks;
+    const int C = (int)min((long long)a.C, blocks0);
+    if (tid == 0) *a.head = PrefixHead{blocks0, C};
+    for (int c = tid; c < a.C; c += N) a.walks[c] = c < C ? prefix_start(a, c, blocks0, C) : PrefixWalk{};
 }
 
 // ---------------------------------------------------------------- tensor memory
@@ -366,7 +353,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
     }
     if (warp == kPfxSoft + 1) tc_alloc(&tmem_slot, 512);
     pdl_enter();
-    if (tid == 0) start = prefix_start(a, blockIdx.x);
+    if (tid == 0) start = a.walks[blockIdx.x];
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -412,20 +399,19 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
         };
-        int seg = 0, s_n = 0;
-        if (w.left > 0) {
+        int seg = 0, s_n = 0, k, n;
+        bool more = prefix_segment(a, w, k, n);
+        if (more) {
             load_q();
             stage_q();
             bar_softmax();
         }
-        while (w.left > 0) {
+        while (more) {
             const PrefixGroup& G = a.groups[w.j];
-            const int n = (int)min((long long)(G.blocks - w.k), w.left);
             const int rows = min(kPfxRows, G.rows - w.t * kPfxRows);
             // tokens from this warp's first column of the first block to the end of the shared pages
-            const int ahead = (int)min((long long)G.pages * PS - (long long)w.k * kPfxTok - half * 32, 0x7fffffffll);
+            const int ahead = (int)min((long long)G.pages * PS - (long long)k * kPfxTok - half * 32, 0x7fffffffll);
             const long long part_row = prefix_part_row(a, G, w.g, w.t, blockIdx.x);
-            if (tid == 0) prefix_note_span(a, w, G, blockIdx.x);
 
             float m = -INFINITY, l = 0.f;
             for (int i = set; i < n; i += 2, ++s_n) {
@@ -493,13 +479,15 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                 if (lane == 0) mbar_arrive(&p_full[set]);
             }
             // the next unit's query goes out before this unit's results: its first products run meanwhile
-            prefix_advance(a, w, n);
-            if (w.left > 0) load_q();
+            const bool two = n > 1;
+            prefix_advance(a, w);
+            more = prefix_segment(a, w, k, n);
+            if (more) load_q();
             const bool ok = pfx_wait(&o_full, seg & 1, &dead, status);
             tc_fence_after();
             ml[quarter][row] = make_float2(m, l);
             bar_softmax();                             // also: nobody reads this unit's maxima any more
-            if (w.left > 0) stage_q();
+            if (more) stage_q();
             // join the two accumulators: a warp takes D/4 columns of its rows
             if (ok && quad * 32 < rows) {
                 const float m0 = ml[0][row].x, m1 = ml[2][row].x;
@@ -511,7 +499,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                 for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
                     uint32_t x[16], y[16] = {};
                     tc_ld16(O[0] + lanes + c, x);
-                    if (n > 1) tc_ld16(O[1] + lanes + c, y);
+                    if (two) tc_ld16(O[1] + lanes + c, y);
                     tc_wait_ld<16>(x);
                     tc_wait_ld<16>(y);
                     if (row < rows)
@@ -521,7 +509,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 o[q] = __uint_as_float(x[e + q]) * f0;
-                                if (n > 1) o[q] = fmaf(__uint_as_float(y[e + q]), f1, o[q]);
+                                if (two) o[q] = fmaf(__uint_as_float(y[e + q]), f1, o[q]);
                             }
                             dst[(c + e) / 4 * rows] = make_float4(o[0], o[1], o[2], o[3]);
                         }
@@ -555,9 +543,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             return go;
         };
         bool go = true;
-        while (w.left > 0 && go) {
+        for (int k, n; go && prefix_segment(a, w, k, n); prefix_advance(a, w)) {
             const PrefixGroup& G = a.groups[w.j];
-            const int n = (int)min((long long)(G.blocks - w.k), w.left), g = w.g;
+            const int g = w.g;
             const int32_t* pages = a.r.page_table + (size_t)G.first * a.r.max_pages;
             // 32 blocks' pages at a time would hide their loads; one block ahead does, behind the ring
             auto page = [&](int blk) {
@@ -573,15 +561,14 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                 }
                 return ph;
             };
-            int ph = page(w.k), prev = -1;
+            int ph = page(k), prev = -1;
             for (int i = 0; i <= n && go; ++i) {
-                const int next = i + 1 < n ? page(w.k + i + 1) : -1;
+                const int next = i + 1 < n ? page(k + i + 1) : -1;
                 if (i < n) go = load(&kmap, g, ph);
                 if (i > 0 && go) go = load(&vmap, g, prev);
                 prev = ph;
                 ph = next;
             }
-            prefix_advance(a, w, n);
         }
         if (!go && lane == 0)
             for (int i = max(0, it - SLOTS); i < it; ++i)
@@ -634,8 +621,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             __syncwarp();
             next_slot();
         };
-        while (uniform(w.left > 0)) {
-            const int n = uniform((int)min((long long)(a.groups[w.j].blocks - w.k), w.left));
+        for (int k, n; uniform(prefix_segment(a, w, k, n)); prefix_advance(a, w)) {
+            n = uniform(n);
             pfx_wait(&q_full, seg & 1, &dead, status);
             tc_fence_after();
             // S0, then S1 V0, S0 V1, ...: each set's scores are made while the other's weights are
@@ -657,7 +644,6 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             if (__all_sync(0xffffffffu, !dead) && elect_one()) tc_commit(&o_full);
             __syncwarp();
             ++seg;
-            prefix_advance(a, w, n);
         }
     }
     tc_fence_before();
@@ -668,74 +654,45 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
 
 // ---------------------------------------------------------------- merge
 // One CTA a (sequence, kv head): the prefix partials in CTA order, then its own.
+constexpr int kPrefixMergeThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a)
+__global__ void __launch_bounds__(kPrefixMergeThreads, 4) prefix_merge_kernel(const PrefixArgs a)
 {
     pdl_enter();
     const RangeArgs& r = a.r;
     const int u = blockIdx.x, b = u / r.H_kv, g = u % r.H_kv;
+    const int h = threadIdx.x % r.G, d4 = threadIdx.x / r.G % (D / 4);   // a tile's partials lie [D / 4][rows] float4
+    const int2 own = r.span[u];
+    const PrefixHead head = *a.head;
     const SeqSpan sp = seq_span(r, b, a.ps, false);
     const int j = a.gid[b];
-    int n_own = 0, n_pfx = 0;
-    int rows = 0, row0 = 0;                            // rows of its tile, and its first among them
-    long long own0 = 0, pfx0 = 0;
-    if (sp.pages() > 0) {
-        const int2 s = r.span[u];
-        n_own = s.y - s.x + 1;
-        own0 = ((long long)s.x + u) * r.G;
-    }
+    PartList list[2] = {};
     if (sp.L > 0 && j >= 0 && a.groups[j].pages > 0) {
         const PrefixGroup G = a.groups[j];
         const int row = (b - G.lo) * r.G, t = row / a.row_tile;
-        const int2 s = a.span[prefix_unit(G, g, t)];
-        n_pfx = s.y - s.x + 1;
-        pfx0 = prefix_part_row(a, G, g, t, s.x);
-        row0 = row % a.row_tile;
-        rows = min(a.row_tile, G.rows - t * a.row_tile);
+        const int2 s = prefix_span(G, g, t, head.total, head.C);
+        const long long base = prefix_part_row(a, G, g, t, s.x);
+        const int rows = min(a.row_tile, G.rows - t * a.row_tile), at = row % a.row_tile + h;
+        list[0] = PartList{reinterpret_cast<const float4*>(a.part_o + base * D) + d4 * rows + at,
+                           reinterpret_cast<const float2*>(a.part_ml) + base + at, a.row_tile, s.y - s.x + 1};
     }
-    for (int i = threadIdx.x; i < r.G * D / 4; i += blockDim.x) {
-        const int h = i & (r.G - 1), d4 = i / r.G;     // a tile's partials lie [D / 4][rows] float4
-        float M = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        // n partials, `step` rows apart; a row's maximum and sum lie at ml + its row
-        auto add = [&](const float* po, const float* pml, long long step, int n) {
-            const float4* p4 = reinterpret_cast<const float4*>(po);
-            const float2* p2 = reinterpret_cast<const float2*>(pml);
-            for (int s0 = 0; s0 < n; s0 += 8) {
-                float4 t[8];
-                float2 ml[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (s0 + k < n) {
-                        t[k] = p4[(s0 + k) * step * (D / 4)];
-                        ml[k] = p2[(s0 + k) * step];
-                    }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (s0 + k < n && ml[k].x != -INFINITY) {
-                        const float mn = fmaxf(M, ml[k].x);
-                        const float f = exp2f(M - mn), e = exp2f(ml[k].x - mn);
-                        M = mn;
-                        l = l * f + ml[k].y * e;
-                        o.x = o.x * f + t[k].x * e;
-                        o.y = o.y * f + t[k].y * e;
-                        o.z = o.z * f + t[k].z * e;
-                        o.w = o.w * f + t[k].w * e;
-                    }
-            }
-        };
-        add(a.part_o + pfx0 * D + ((long long)d4 * rows + row0 + h) * 4, a.part_ml + (pfx0 + row0 + h) * 2, a.row_tile,
-            n_pfx);
-        add(r.part_o + (own0 + h) * D + d4 * 4, r.part_ml + (own0 + h) * 2, r.G, n_own);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t row = (size_t)b * r.H_q + (size_t)g * r.G + h;
-        float* dst = r.out + row * D + d4 * 4;
-        dst[0] = o.x * inv;
-        dst[1] = o.y * inv;
-        dst[2] = o.z * inv;
-        dst[3] = o.w * inv;
-        if (d4 == 0 && r.lse) r.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    if (sp.pages() > 0) {
+        const long long row = ((long long)own.x + u) * r.G + h;
+        list[1] = PartList{reinterpret_cast<const float4*>(r.part_o + row * D) + d4,
+                           reinterpret_cast<const float2*>(r.part_ml) + row, r.G, own.y - own.x + 1};
     }
+    float4 o;
+    float m, l;
+    if (!merge_parts<D, kPrefixMergeThreads>(list[0], list[1], r.G, o, m, l)) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t row = (size_t)b * r.H_q + (size_t)g * r.G + h;
+    float* dst = r.out + row * D + d4 * 4;
+    dst[0] = o.x * inv;
+    dst[1] = o.y * inv;
+    dst[2] = o.z * inv;
+    dst[3] = o.w * inv;
+    if (d4 == 0 && r.lse) r.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -768,8 +725,8 @@ int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, c
     if (rc) return rc;
     if ((rc = launch_range(pool, a.r, range_C, kmap, vmap, stream))) return rc;
     const dim3 grid(a.r.B * a.r.H_kv);
-    const cudaError_t e = pool.d == 128 ? launch_pdl(prefix_merge_kernel<128>, grid, dim3(128), 0, stream, a)
-                                        : launch_pdl(prefix_merge_kernel<64>, grid, dim3(128), 0, stream, a);
+    const cudaError_t e = pool.d == 128 ? launch_pdl(prefix_merge_kernel<128>, grid, dim3(kPrefixMergeThreads), 0, stream, a)
+                                        : launch_pdl(prefix_merge_kernel<64>, grid, dim3(kPrefixMergeThreads), 0, stream, a);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 

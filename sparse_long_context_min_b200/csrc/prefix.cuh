@@ -13,9 +13,19 @@ struct PrefixGroup {
     int pages;                 // whole pages that the group shares (0: nothing is shared)
     int rows, tiles;           // query rows of one kv head (n * G), and row tiles
     int blocks;                // token blocks of the shared pages
-    int unit0;                 // first unit: (kv head, row tile) in this order
-    long long row0;            // partial rows of all units before
+    long long row0;            // partial rows of all units before ((kv head, row tile) in this order)
     long long block0;          // blocks of all units before
+};
+
+struct PrefixHead {
+    long long total;           // blocks of all units
+    int C;                     // CTAs that have a share of them
+};
+
+// A CTA's place in its share: group, kv head, row tile, block, and what is left.
+struct PrefixWalk {
+    int j, g, t, k;
+    long long left;
 };
 
 struct PrefixArgs {
@@ -29,28 +39,26 @@ struct PrefixArgs {
     int32_t* shared;           // [B] first page of each sequence's own range
     int32_t* gid;              // [B] group of each sequence, -1 without one
     PrefixGroup* groups;       // [n_groups]
-    long long* total;          // blocks of all units
-    int2* span;                // [units] first and last CTA of a unit
-    float* part_o;             // [rows][d]: a unit's rows of CTA c start at its row0 + row_tile * c
+    PrefixHead* head;
+    PrefixWalk* walks;         // [C] each CTA's share
+    float* part_o;             // partials of (CTA c, unit): [d / 4][the unit's rows] float4 from row prefix_part_row on
     float* part_ml;            // [rows][2]
 };
 
 // The units of all groups laid end to end, dealt to the CTAs in equal shares.
-struct PrefixWalk {
-    int j, g, t, k;            // group, kv head, row tile, next block
-    int C;
-    long long left, total;
-};
+// To start a unit costs a CTA about as long as kPrefixTurn blocks (its query,
+// the end of the pipeline before, its results): every unit is laid out with as
+// many blocks in front that hold no work.
+constexpr int kPrefixTurn = 4;
+
+EKV_DEV int prefix_len(const PrefixGroup& G) { return G.blocks + kPrefixTurn; }
 
 // One thread: CTA c's share.
-EKV_DEV PrefixWalk prefix_start(const PrefixArgs& a, int c)
+EKV_DEV PrefixWalk prefix_start(const PrefixArgs& a, int c, long long total, int C)
 {
     PrefixWalk w{};
-    w.total = *a.total;
-    w.C = (int)min((long long)a.C, w.total);
-    if (c >= w.C) return w;
-    const long long b0 = w.total * c / w.C;
-    w.left = w.total * (c + 1) / w.C - b0;
+    const long long b0 = mul_div(total, c, C);
+    w.left = mul_div(total, c + 1, C) - b0;
     int lo = 0, hi = a.n_groups - 1;                   // last group with block0 <= b0 and blocks in it
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -58,30 +66,39 @@ EKV_DEV PrefixWalk prefix_start(const PrefixArgs& a, int c)
         else hi = mid - 1;
     }
     const PrefixGroup& G = a.groups[lo];
-    const long long in = b0 - G.block0;
+    const int len = prefix_len(G);
+    const long long in = b0 - G.block0, unit = in < (1ll << 31) ? (int)in / len : in / len;
     w.j = lo;
-    w.k = (int)(in % G.blocks);
-    w.g = (int)(in / G.blocks / G.tiles);
-    w.t = (int)(in / G.blocks % G.tiles);
+    w.k = (int)(in - unit * len);
+    w.g = (int)unit / G.tiles;                         // units of a group: 31 bits
+    w.t = (int)unit % G.tiles;
     return w;
 }
 
-// Past n blocks of the current unit (at most to its end).
-EKV_DEV void prefix_advance(const PrefixArgs& a, PrefixWalk& w, int n)
+// What a CTA does of its current unit: blocks [k, k + n).  False at the end of
+// its share (blocks without work may be left of it).
+EKV_DEV bool prefix_segment(const PrefixArgs& a, const PrefixWalk& w, int& k, int& n)
 {
-    w.k += n;
-    w.left -= n;
-    if (w.left <= 0 || w.k < a.groups[w.j].blocks) return;
+    if (w.left <= kPrefixTurn - w.k || w.left <= 0) return false;
+    const long long end = min((long long)prefix_len(a.groups[w.j]), w.k + w.left) - kPrefixTurn;
+    k = max(w.k - kPrefixTurn, 0);
+    n = (int)end - k;
+    return true;
+}
+
+// To the next unit.
+EKV_DEV void prefix_advance(const PrefixArgs& a, PrefixWalk& w)
+{
+    const PrefixGroup& G = a.groups[w.j];
+    w.left -= prefix_len(G) - w.k;
     w.k = 0;
-    if (++w.t < a.groups[w.j].tiles) return;
+    if (w.left <= 0 || ++w.t < G.tiles) return;
     w.t = 0;
     if (++w.g < a.r.H_kv) return;
     w.g = 0;
     do ++w.j;
     while (a.groups[w.j].pages == 0);
 }
-
-EKV_DEV int prefix_unit(const PrefixGroup& G, int g, int t) { return G.unit0 + g * G.tiles + t; }
 
 // First partial row of unit (g, t) of a group at CTA c: units' rows and CTAs
 // form a staircase, so the ranges of two (CTA, unit) pairs never meet.
@@ -90,13 +107,11 @@ EKV_DEV long long prefix_part_row(const PrefixArgs& a, const PrefixGroup& G, int
     return G.row0 + (long long)g * G.rows + (long long)t * a.row_tile + (long long)a.row_tile * c;
 }
 
-// The CTA that holds a unit's first block leaves its CTAs for the merge.
-EKV_DEV void prefix_note_span(const PrefixArgs& a, const PrefixWalk& w, const PrefixGroup& G, int c)
+// First and last CTA that hold blocks of unit (g, t).
+EKV_DEV int2 prefix_span(const PrefixGroup& G, int g, int t, long long total, int C)
 {
-    if (w.k != 0) return;
-    const int u = prefix_unit(G, w.g, w.t);
-    const long long at = G.block0 + (long long)(u - G.unit0) * G.blocks;
-    a.span[u] = make_int2(c, range_cta_of(at + G.blocks - 1, w.total, w.C));
+    const long long at = G.block0 + ((long long)g * G.tiles + t) * prefix_len(G);
+    return make_int2(range_cta_of(at + kPrefixTurn, total, C), range_cta_of(at + prefix_len(G) - 1, total, C));
 }
 
 int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, const CUtensorMap* kmap,

@@ -27,6 +27,8 @@ struct RangeArgs {
     int B;
     int num_phys;
     int window, sinks;             // window form: tokens < sinks and >= L - window
+    const int32_t* group_start;    // [n_groups + 1] bounds to check only (groups too small to share), or NULL
+    int n_groups;
     const int32_t* shared;         // [B] prefix form: first page of each sequence's own range, else NULL
     float xscale;                  // scale * log2(e): scores are kept in the base-2 domain
     float* part_o;                 // [CTAs + units][G][d] partial outputs
@@ -78,6 +80,14 @@ EKV_DEV SeqSpan seq_span(const RangeArgs& a, int b, int ps, bool rep)
     return r;
 }
 
+// a * b / c for a >= 0 and b, c in [0, 2^16); 64-bit division costs several times
+// the 32-bit one, and nearly every total is small.
+EKV_DEV long long mul_div(long long a, int b, int c)
+{
+    if (a < (1ll << 31) / max(b, 1)) return (int)a * b / c;
+    return a * b / c;
+}
+
 // A CTA's share of the tiles: starts at tile t of unit (b, g), `left` tiles;
 // C is the number of CTAs that have a share (each at least one tile).
 struct RangeWalk {
@@ -99,6 +109,11 @@ EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
         if (b == tid) first = t;
         mine += t;
     }
+    if (c == 0 && a.group_start)
+        for (int j = tid; j <= a.n_groups; j += n) {
+            const int s = a.group_start[j];
+            if (s < 0 || s > a.B || (j > 0 && s < a.group_start[j - 1])) report(a.status, ENTMAXKV_DEVICE_BOUNDS);
+        }
     const long long sum = warp_sum(mine);
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
@@ -111,8 +126,8 @@ EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
     w.left = 0;
     w.b = w.g = w.t = 0;
     if (c >= C) return w;
-    const long long t0 = total * c / C;
-    w.left = total * (c + 1) / C - t0;
+    const long long t0 = mul_div(total, c, C);
+    w.left = mul_div(total, c + 1, C) - t0;
     // the sequence that holds tile t0: chunks of blockDim sequences in turn
     long long before = 0;
     for (int base = 0; base < a.B; base += n) {
@@ -150,6 +165,72 @@ EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
 }
 
 // The CTA whose share holds tile `at` of all tiles.
-EKV_DEV int range_cta_of(long long at, long long total, int C) { return (int)(((at + 1) * C - 1) / total); }
+EKV_DEV int range_cta_of(long long at, long long total, int C)
+{
+    const long long x = (at + 1) * C - 1;
+    return x < (1ll << 32) && total < (1ll << 32) ? (int)((uint32_t)x / (uint32_t)total) : (int)(x / total);
+}
+
+// Partial results of rows, one after the other: of partial s the row's maximum
+// and sum lie at ml[s * step] and its four output dims at o[s * step * D / 4].
+struct PartList {
+    const float4* o;
+    const float2* ml;
+    long long step;
+    int n;
+};
+
+// Joins the partials of list x, then those of list y, of G rows of D dims: the
+// block's threads form teams of G * D / 4 (one float4 of one row a thread),
+// team t takes the partials t, t + teams, ... and the teams' results are joined
+// in their order.  The first team's threads return true with the row's output
+// (not yet divided by l), maximum and sum.  All threads of the block call.
+template <int D, int THREADS>
+EKV_DEV bool merge_parts(const PartList& x, const PartList& y, int G, float4& o, float& m, float& l)
+{
+    __shared__ float4 so[THREADS];
+    __shared__ float2 sml[THREADS];
+    const int items = G * (D / 4), teams = THREADS / items, team = threadIdx.x / items;
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](float4 t, float2 ml) {
+        if (ml.x == -INFINITY) return;
+        const float mn = fmaxf(m, ml.x);
+        const float f = exp2f(m - mn), e = exp2f(ml.x - mn);
+        m = mn;
+        l = l * f + ml.y * e;
+        o.x = o.x * f + t.x * e;
+        o.y = o.y * f + t.y * e;
+        o.z = o.z * f + t.z * e;
+        o.w = o.w * f + t.w * e;
+    };
+    const int n = x.n + y.n;
+    for (int s0 = team; s0 < n; s0 += 4 * teams) {
+        float4 t[4];
+        float2 ml[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int s = s0 + k * teams;
+            if (s < n) {
+                const PartList& p = s < x.n ? x : y;
+                const long long at = (s < x.n ? s : s - x.n) * p.step;
+                t[k] = p.o[at * (D / 4)];
+                ml[k] = p.ml[at];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s0 + k * teams < n) join(t[k], ml[k]);
+    }
+    if (teams > 1 && n > 1) {
+        so[threadIdx.x] = o;
+        sml[threadIdx.x] = make_float2(m, l);
+        __syncthreads();
+        if (team == 0)
+            for (int k = 1; k < min(teams, n); ++k) join(so[threadIdx.x + k * items], sml[threadIdx.x + k * items]);
+    }
+    return team == 0;
+}
 
 }  // namespace ekv

@@ -69,7 +69,7 @@ EKV_DEV void range_store(const RangeArgs& a, bool whole, long long slot, int b, 
 EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int nt, int done, int c)
 {
     if (w.t != 0) return;
-    const long long at = w.total * c / w.C + done;     // this unit's first tile among all tiles
+    const long long at = mul_div(w.total, c, w.C) + done;     // this unit's first tile among all tiles
     a.span[u] = make_int2(c, range_cta_of(at + nt - 1, w.total, w.C));
 }
 
@@ -504,47 +504,26 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------- merge
-// One CTA a unit: rows of a unit that several CTAs share are joined in CTA
-// order; rows of a unit without tokens get o = 0 and lse = -infinity.
+// One CTA a unit: rows of a unit that several CTAs share are joined; rows of a
+// unit without tokens get o = 0 and lse = -infinity.
+constexpr int kMergeThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(128) range_merge_kernel(int ps, const RangeArgs a)
+__global__ void __launch_bounds__(kMergeThreads, 4) range_merge_kernel(int ps, const RangeArgs a)
 {
     pdl_enter();
-    const int u = blockIdx.x, b = u / a.H_kv, g = u % a.H_kv, tid = threadIdx.x;
+    const int u = blockIdx.x, b = u / a.H_kv, g = u % a.H_kv;
     const int2 sp = a.span[u];
     const bool empty = seq_span(a, b, ps, false).pages() == 0;
     if (!empty && sp.x == sp.y) return;
-    const int S = empty ? 0 : sp.y - sp.x + 1;
-    for (int i = tid; i < a.G * D / 4; i += blockDim.x) {
-        const int h = i / (D / 4), d = i % (D / 4) * 4;
-        const size_t row0 = ((size_t)sp.x + u) * a.G + h;
-        float M = -INFINITY;
-        for (int s = 0; s < S; ++s) M = fmaxf(M, a.part_ml[(row0 + (size_t)s * a.G) * 2]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        for (int s0 = 0; s0 < S; s0 += 8) {
-            float4 t[8];
-            float2 ml[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (s0 + k < S) {
-                    const size_t row = row0 + (size_t)(s0 + k) * a.G;
-                    t[k] = *reinterpret_cast<const float4*>(a.part_o + row * D + d);
-                    ml[k] = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
-                }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (s0 + k < S && ml[k].x != -INFINITY) {
-                    const float f = exp2f(ml[k].x - M);
-                    l = fmaf(ml[k].y, f, l);
-                    o.x = fmaf(t[k].x, f, o.x);
-                    o.y = fmaf(t[k].y, f, o.y);
-                    o.z = fmaf(t[k].z, f, o.z);
-                    o.w = fmaf(t[k].w, f, o.w);
-                }
-        }
-        range_store(a, true, 0, b, g, h, D, d, o, M, l);
-    }
+    const int h = threadIdx.x / (D / 4) % a.G, d = threadIdx.x % (D / 4) * 4;
+    const size_t row = ((size_t)sp.x + u) * a.G + h;
+    const PartList list{reinterpret_cast<const float4*>(a.part_o + (empty ? 0 : row * D + d)),
+                        reinterpret_cast<const float2*>(a.part_ml) + (empty ? 0 : row), a.G,
+                        empty ? 0 : sp.y - sp.x + 1};
+    float4 o;
+    float m, l;
+    if (merge_parts<D, kMergeThreads>(list, PartList{}, a.G, o, m, l)) range_store(a, true, 0, b, g, h, D, d, o, m, l);
 }
 
 // ---------------------------------------------------------------- launch
@@ -591,8 +570,8 @@ int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CU
     if (rc) return rc;
     const dim3 grid(a.B * a.H_kv);
     const cudaError_t e = pool.d == 128
-                              ? launch_pdl(range_merge_kernel<128>, grid, dim3(128), 0, stream, pool.ps, a)
-                              : launch_pdl(range_merge_kernel<64>, grid, dim3(128), 0, stream, pool.ps, a);
+                              ? launch_pdl(range_merge_kernel<128>, grid, dim3(kMergeThreads), 0, stream, pool.ps, a)
+                              : launch_pdl(range_merge_kernel<64>, grid, dim3(kMergeThreads), 0, stream, pool.ps, a);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 

@@ -3,6 +3,7 @@
 The pages of a group's prefix are shared in its page-table rows; everything that
 a call must not use holds NaN or infinity.
 """
+import itertools
 import math
 
 import numpy as np
@@ -20,9 +21,11 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 class Shared(Cache):
     """groups: (prefix length, lengths of its sequences); a sequence shorter than the
-    prefix holds only its first tokens."""
+    prefix holds only its first tokens.  With `wide` the table's rows are so long
+    that the library shares the prefix's reading (small calls read it for each
+    sequence)."""
 
-    def __init__(self, groups, H_q, H_kv, d, ps, dtype, seed=0, spread=1.0):
+    def __init__(self, groups, H_q, H_kv, d, ps, dtype, seed=0, spread=1.0, wide=True):
         lens = [L for _, ls in groups for L in ls]
         super().__init__(lens, H_q, H_kv, d, ps, dtype, seed=seed, spread=spread)
         table = self.table.cpu()
@@ -43,6 +46,10 @@ class Shared(Cache):
             b += len(ls)
             self.starts.append(b)
             self.prefixes.append(prefix)
+        if wide:
+            entries = (64 << 20) // (ps * H_kv * d * 2 * (2 if dtype == BF16 else 4)) + 1
+            pad = max(0, -(-entries // max(len(lens), 1)) - table.shape[1])
+            table = torch.cat([table, torch.full((len(lens), pad), -1, dtype=torch.int32)], dim=1)
         self.table = table.cuda()
 
     def run(self, workspace=None, out=None, lse=None, stream=None, starts=None, prefixes=None):
@@ -72,8 +79,9 @@ SHAPES = [(32, 8, 128, 64, BF16), (4, 4, 64, 16, BF16), (4, 1, 64, 16, F32), (8,
 @pytest.mark.parametrize("prefix", [0, 1, 16, 65, 128, 129, 700])
 def test_prefix_matches_definition(H_q, H_kv, d, ps, dtype, prefix):
     tails = [1, 0, 17, 64, 300]
-    c = Shared([(prefix, [prefix + t for t in tails])], H_q, H_kv, d, ps, dtype, seed=prefix)
-    c.verify()
+    for wide in (True, False):
+        c = Shared([(prefix, [prefix + t for t in tails])], H_q, H_kv, d, ps, dtype, seed=prefix, wide=wide)
+        c.verify()
 
 
 @pytest.mark.parametrize("H_q,H_kv,d,ps,dtype", SHAPES[:4])
@@ -113,8 +121,8 @@ def test_first_row_of_a_group_has_left():
 
 def test_bad_groups_and_pages_are_reported():
     i32 = dict(dtype=torch.int32, device="cuda")
-    for starts in ([0, 6], [-1, 3], [4, 2], [0, 4, 0, 4, 0]):
-        c = Shared([(300, [400, 350, 420, 310])], 8, 2, 64, 16, BF16, seed=5)
+    for starts, wide in itertools.product(([0, 6], [-1, 3], [4, 2], [0, 4, 0, 4, 0]), (True, False)):
+        c = Shared([(300, [400, 350, 420, 310])], 8, 2, 64, 16, BF16, seed=5, wide=wide)
         prefixes = torch.tensor([300] * (len(starts) - 1), **i32)
         out, lse = c.run(starts=torch.tensor(starts, **i32), prefixes=prefixes)
         torch.cuda.synchronize()
