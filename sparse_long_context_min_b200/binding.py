@@ -100,7 +100,7 @@ def _check(rc, where):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 class _Args:
@@ -111,12 +111,23 @@ class _Args:
     layout of each tensor as it is named and `reachable` then checks that every
     one is the current device's memory or pinned (mapped) host memory."""
 
+    __slots__ = ("where", "dev", "far")
+
     def __init__(self, where):
         self.where = where
-        self.seen = []
+        self.dev = None
+        self.far = None                                # tensors that are not on the current device
 
     def fail(self, detail, code=INVALID_ARG):
         raise EntmaxKVError(code, self.where, detail)
+
+    def pool(self, pool):
+        """The pool's memory belongs to the device that was current when it was made."""
+        if pool.index >= 0:
+            if self.dev is None:
+                self.dev = torch.cuda.current_device()
+            if pool.index != self.dev:
+                self.fail("the pool is on cuda:%d, the current device is cuda:%d" % (pool.index, self.dev))
 
     def need(self, t, name, dtype=None, numel=0, dims=None):
         if t is None:
@@ -129,17 +140,19 @@ class _Args:
             self.fail("%s must be contiguous" % name)
         if t.numel() < numel:
             self.fail("%s holds %d elements; the call addresses %d" % (name, t.numel(), numel))
-        self.seen.append((name, t))
+        index = t.get_device()                         # -1: host memory
+        if index != self.dev or index < 0:
+            if index >= 0 and self.dev is None:
+                self.dev = torch.cuda.current_device()
+            if index != self.dev or index < 0:
+                self.far = (self.far or []) + [(name, t)]
         return t
 
     def reachable(self):
-        dev = capturing = None
-        for name, t in self.seen:
+        capturing = None
+        for name, t in self.far or ():
             if t.is_cuda:
-                dev = torch.cuda.current_device() if dev is None else dev
-                if t.get_device() != dev:
-                    self.fail("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), dev))
-                continue
+                self.fail("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), self.dev))
             if capturing is None:
                 # the pinned-memory query is not issued while a CUDA graph is
                 # being captured; the eager call before a capture checks it
@@ -148,9 +161,16 @@ class _Args:
                 self.fail("%s must be in device memory or pinned host memory" % name)
 
 
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 class Pool:
@@ -184,6 +204,8 @@ class Pool:
         self._c = CPool(k_pool.data_ptr(), v_pool.data_ptr(), kmin.data_ptr(), kmax.data_ptr(),
                         mean.data_ptr(), m2.data_ptr(), count.data_ptr(), self.num_phys, self.H_kv,
                         self.ps, self.d, self.dtype)
+        self.c = ctypes.byref(self._c)
+        self.index = k_pool.get_device()
 
     @classmethod
     def allocate(cls, num_phys, H_kv, ps, d, dtype=torch.bfloat16, device="cuda"):
@@ -194,9 +216,6 @@ class Pool:
                    torch.zeros(num_phys, H_kv, d, **f32), torch.zeros(num_phys, H_kv, d, **f32),
                    torch.zeros(num_phys, dtype=torch.int32, device=device))
 
-    @property
-    def c(self):
-        return ctypes.byref(self._c)
 
 
 I32, F32T = torch.int32, torch.float32
@@ -204,6 +223,7 @@ I32, F32T = torch.int32, torch.float32
 
 def _query(a, pool, q):
     """q [B, H_q, d] float32 with the pool's d; returns (B, H_q)."""
+    a.pool(pool)
     a.need(q, "q", F32T, dims=3)
     if q.shape[2] != pool.d:
         a.fail("q has %d dims per head, the pool %d" % (q.shape[2], pool.d))
@@ -244,6 +264,7 @@ def _bytes(t):
 def append_metadata(pool, k_new, v_new, page_table, seq_lens, status, stream=None):
     """k_new, v_new [B, H_kv, n_new, d]; seq_lens advanced in place on the device."""
     a = _Args("append_metadata")
+    a.pool(pool)
     a.need(k_new, "k_new", pool.k_pool.dtype, dims=4)
     B, H_kv, n_new, d = k_new.shape
     if H_kv != pool.H_kv or d != pool.d:
@@ -439,6 +460,7 @@ def prefix_softmax_decode(pool, q, page_table, seq_lens, group_start, prefix_len
 def _owned(a, pool, ref, page_table, seq_lens):
     """A reference-counted table: ref [num_phys], page_table [B, max_pages] and
     seq_lens [B] (None where the call takes none), int32; returns (B, max_pages)."""
+    a.pool(pool)
     a.need(ref, "ref", I32, pool.num_phys)
     a.need(page_table, "page_table", I32, dims=2)
     B, max_pages = page_table.shape
@@ -459,6 +481,7 @@ def _pairs(a, src, dst):
 def copy_pages(pool, src, dst, workspace, status, stream=None):
     """Page dst[i] becomes page src[i], keys, values and metadata (workspace: OP_PAGES)."""
     a = _Args("copy_pages")
+    a.pool(pool)
     n = _pairs(a, src, dst)
     a.need(workspace, "workspace")
     a.need(status, "status", I32, 1)

@@ -355,6 +355,22 @@ static RangeArgs range_args(const entmaxkv_pool& pool, const float* q, int H_q, 
     return a;
 }
 
+// The range kernels over at most `pages` pages a sequence.  Few and short
+// units: a cluster of CTAs each, joined in shared memory, one launch.  Else
+// equal shares of all tiles for two CTAs an SM, and a merge launch.  A cluster
+// has as many CTAs as leave each two tiles, as far as all of them fit the GPU at
+// once; where that leaves a CTA more than 8 tiles, the bytes bound the time and
+// equal shares over all SMs are faster.
+static int launch_ranges(const entmaxkv_pool& pool, const RangeArgs& a, int C, long long pages, const CUtensorMap* kmap,
+                         const CUtensorMap* vmap, cudaStream_t stream)
+{
+    const long long tiles = (pages * pool.ps + kRangeTile - 1) / kRangeTile, units = (long long)a.B * a.H_kv;
+    int n = 1;
+    while (n < 16 && (tiles + n - 1) / n > 2 && units * 2 * n <= 256) n *= 2;
+    if ((tiles + n - 1) / n <= 8 && units * n <= 256) return launch_window_cluster(pool, a, n, kmap, vmap, stream);
+    return launch_window(pool, a, (int)std::min((long long)C, tiles * units), kmap, vmap, stream);
+}
+
 struct PrefixLayout {
     RangeLayout range;
     int C;
@@ -567,12 +583,9 @@ int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const float* q, in
         if ((rc = make_pool_map(&kmap, *pool, pool->k_pool))) return rc;
         if ((rc = make_pool_map(&vmap, *pool, pool->v_pool))) return rc;
     }
-    // no more CTAs than the longest possible ranges have tiles
     const long long pages = std::min((long long)max_pages, ((long long)sinks + pool->ps - 1) / pool->ps +
                                                                ((long long)window + pool->ps - 1) / pool->ps + 1);
-    const long long tiles = (pages * pool->ps + kRangeTile - 1) / kRangeTile * B * pool->H_kv;
-    return launch_window(*pool, a, (int)std::min((long long)lay.C, tiles), &kmap, &vmap,
-                         static_cast<cudaStream_t>(stream));
+    return launch_ranges(*pool, a, lay.C, pages, &kmap, &vmap, static_cast<cudaStream_t>(stream));
 }
 
 int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, int32_t H_q, const int32_t* page_table,
@@ -601,9 +614,7 @@ int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, in
         a.r.direct = 1;
         a.r.group_start = n_groups ? group_start : nullptr;
         a.r.n_groups = n_groups;
-        const long long tiles = ((long long)max_pages * pool->ps + kRangeTile - 1) / kRangeTile * B * pool->H_kv;
-        return launch_window(*pool, a.r, (int)std::min((long long)lay.range.C, tiles), &kmap, &vmap,
-                             static_cast<cudaStream_t>(stream));
+        return launch_ranges(*pool, a.r, lay.range.C, max_pages, &kmap, &vmap, static_cast<cudaStream_t>(stream));
     }
     a.group_start = group_start;
     a.prefix_lens = prefix_lens;

@@ -46,6 +46,14 @@ int launch_range(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUt
 // The same, and the merge of units that CTAs share.
 int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream);
+// The same as one launch, a cluster of `cluster` CTAs a unit.
+int launch_window_cluster(const entmaxkv_pool& pool, const RangeArgs& a, int cluster, const CUtensorMap* kmap,
+                          const CUtensorMap* vmap, cudaStream_t stream);
+
+// x / ps for x >= 0 and the page sizes there are (a division by a variable takes
+// longer than a step of the fp32 kernel)
+template <typename T>
+EKV_DEV T div_ps(T x, int ps) { return ps == 64 ? x >> 6 : x >> 4; }
 
 // The pages a sequence's unit walks: logical pages [0, n1) and [p2, P), tokens
 // valid where pos < s or w0 <= pos < L.
@@ -61,7 +69,7 @@ EKV_DEV SeqSpan seq_span(const RangeArgs& a, int b, int ps, bool rep)
 {
     SeqSpan r;
     r.L = max(a.seq_lens[b], 0);
-    r.P = (int)(((long long)r.L + ps - 1) / ps);
+    r.P = (int)div_ps((long long)r.L + ps - 1, ps);
     if (r.P > a.max_pages) {
         if (rep) report(a.status, ENTMAXKV_DEVICE_BOUNDS);
         r.P = a.max_pages;
@@ -74,8 +82,8 @@ EKV_DEV SeqSpan seq_span(const RangeArgs& a, int b, int ps, bool rep)
     } else {
         r.s = min(a.sinks, r.L);
         r.w0 = max(r.s, r.L - a.window);
-        r.n1 = min((r.s + ps - 1) / ps, r.P);
-        r.p2 = min(max(r.w0 / ps, r.n1), r.P);
+        r.n1 = min((int)div_ps((long long)r.s + ps - 1, ps), r.P);
+        r.p2 = min(max(div_ps(r.w0, ps), r.n1), r.P);
     }
     return r;
 }
@@ -95,6 +103,29 @@ struct RangeWalk {
     long long left, total;
 };
 
+// Bounds of groups that a call does not use otherwise; one block.
+EKV_DEV void range_check_groups(const RangeArgs& a)
+{
+    if (!a.group_start) return;
+    for (int j = threadIdx.x; j <= a.n_groups; j += blockDim.x) {
+        const int s = a.group_start[j];
+        if (s < 0 || s > a.B || (j > 0 && s < a.group_start[j - 1])) report(a.status, ENTMAXKV_DEVICE_BOUNDS);
+    }
+}
+
+// The share of the CTA `r` of a cluster of n that has unit u to itself.
+EKV_DEV RangeWalk range_cluster_start(const RangeArgs& a, int ps, int u, int r, int n)
+{
+    if (u == 0 && r == 0) range_check_groups(a);
+    RangeWalk w{};
+    w.b = u / a.H_kv;
+    w.g = u % a.H_kv;
+    const int nt = seq_span(a, w.b, ps, w.g == 0 && r == 0).tiles(ps);
+    w.t = (int)((long long)nt * r / n);
+    w.left = (int)((long long)nt * (r + 1) / n) - w.t;
+    return w;
+}
+
 // All threads of the block call.
 EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
 {
@@ -109,11 +140,7 @@ EKV_DEV RangeWalk range_start(const RangeArgs& a, int ps, int c, int grid)
         if (b == tid) first = t;
         mine += t;
     }
-    if (c == 0 && a.group_start)
-        for (int j = tid; j <= a.n_groups; j += n) {
-            const int s = a.group_start[j];
-            if (s < 0 || s > a.B || (j > 0 && s < a.group_start[j - 1])) report(a.status, ENTMAXKV_DEVICE_BOUNDS);
-        }
+    if (c == 0) range_check_groups(a);
     const long long sum = warp_sum(mine);
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();

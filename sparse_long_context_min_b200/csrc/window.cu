@@ -64,6 +64,50 @@ EKV_DEV void range_store(const RangeArgs& a, bool whole, long long slot, int b, 
     dst[0] = o.x; dst[1] = o.y; dst[2] = o.z; dst[3] = o.w;
 }
 
+// A CTA's part of its cluster's unit.
+template <int D>
+struct ClusterPart {
+    float o[8][D], m[8], l[8];           // heads of the group
+};
+
+// Joins the cluster's parts in rank order and writes the unit's rows; a CTA
+// takes every n-th group of four dims.  All threads of all CTAs call.
+template <int D>
+EKV_DEV void range_cluster_join(const RangeArgs& a, ClusterPart<D>& part, int b, int g, int r, int n)
+{
+    cluster_sync();
+    for (int i = r + n * (int)threadIdx.x; i < a.G * D / 4; i += n * (int)blockDim.x) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        float M = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < n; c0 += 8) {
+            uint4 t[8];
+            float m[8], s[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c0 + k < n) {
+                    t[k] = ld_dsmem_v4(dsmem(&part.o[h][d], c0 + k));
+                    m[k] = ld_dsmem_f32(dsmem(&part.m[h], c0 + k));
+                    s[k] = ld_dsmem_f32(dsmem(&part.l[h], c0 + k));
+                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c0 + k < n && m[k] != -INFINITY) {
+                    const float mn = fmaxf(M, m[k]);
+                    const float f = exp2f(M - mn), e = exp2f(m[k] - mn);
+                    M = mn;
+                    l = l * f + s[k] * e;
+                    o.x = o.x * f + __uint_as_float(t[k].x) * e;
+                    o.y = o.y * f + __uint_as_float(t[k].y) * e;
+                    o.z = o.z * f + __uint_as_float(t[k].z) * e;
+                    o.w = o.w * f + __uint_as_float(t[k].w) * e;
+                }
+        }
+        range_store(a, true, 0, b, g, h, D, d, o, M, l);
+    }
+    cluster_sync();                      // nobody leaves while its part may still be read
+}
+
 // The CTA that holds a unit's first tile leaves the unit's first and last CTA
 // for the merge.
 EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int nt, int done, int c)
@@ -82,10 +126,10 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // product, its result's layout is turned in registers (movmatrix) into the B
 // operand of V^T P, and P again keeps a high and a low part: both splits leave
 // about 2^-17 of relative error where one bf16 would leave 2^-9.
-template <int D, int PS, int NT>
+template <int D, int PS, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                       const __grid_constant__ CUtensorMap vmap,
-                                                                      const RangeArgs a)
+                                                                      const RangeArgs a, int cluster)
 {
     pdl_enter();
     constexpr int STAGE = kRangeTile * D * 2;          // bytes of one tensor's tile
@@ -109,8 +153,21 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
         fence_mbar_init();
         dead = 0;
     }
-    RangeWalk w = range_start(a, PS, c_id, gridDim.x);         // holds block barriers
-    if (w.left <= 0) return;
+    const int rank = CLUSTER ? c_id % cluster : 0;
+    __shared__ __align__(16) uint8_t part_raw[CLUSTER ? sizeof(ClusterPart<D>) : 16];
+    ClusterPart<D>& part = *reinterpret_cast<ClusterPart<D>*>(part_raw);
+    RangeWalk w;
+    if (CLUSTER) {
+        w = range_cluster_start(a, PS, c_id / cluster, rank, cluster);
+        if (w.left <= 0 && tid < 8) {
+            part.m[tid] = -INFINITY;
+            part.l[tid] = 0.f;
+        }
+    } else {
+        w = range_start(a, PS, c_id, gridDim.x);       // holds block barriers
+        if (w.left <= 0) return;
+    }
+    const int b0 = w.b, g0 = w.g;                      // a cluster's unit
     __syncthreads();
 
     int b = w.b;
@@ -186,7 +243,8 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
         if (stop && lane == 0)
             for (long long i = max(0ll, issued - kRangeStages); i < issued; ++i)
                 mbar_wait(&full[i % kRangeStages], (uint32_t)((i / kRangeStages) & 1), kWaitLimitNs);
-        return;
+        w.left = 0;
+        if (!CLUSTER) return;
     }
 
     // -------------------------------------------------------- consumers
@@ -200,7 +258,7 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
         const int n = (int)min((long long)(nt - w.t), w.left);
         const int u = b * a.H_kv + w.g;
         const bool whole = a.direct && n == nt;
-        if (tid == 0) range_note_span(a, w, u, nt, done, c_id);
+        if (!CLUSTER && tid == 0) range_note_span(a, w, u, nt, done, c_id);
 
         uint32_t bq[NT][KS][2];
 #pragma unroll
@@ -341,33 +399,69 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     const float4 t = *reinterpret_cast<const float4*>(red + (i * 4 + h) * RED + d);
                     o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
                 }
-                range_store(a, whole, (long long)c_id + u, b, w.g, 4 * x + h, D, d, o, Mh, L);
+                if (!CLUSTER) {
+                    range_store(a, whole, (long long)c_id + u, b, w.g, 4 * x + h, D, d, o, Mh, L);
+                } else {
+                    *reinterpret_cast<float4*>(&part.o[4 * x + h][d]) = o;
+                    if (d == 0) {
+                        part.m[4 * x + h] = Mh;
+                        part.l[4 * x + h] = L;
+                    }
+                }
             }
         }
         done += n;
         advance(n);
     }
+    if (CLUSTER) range_cluster_join<D>(a, part, b0, g0, rank, cluster);
 }
 
 // ---------------------------------------------------------------- fp32 cache
-// Each warp owns 16 tokens of a tile and keeps everything in registers: LPT
-// lanes share a token (each holds D / LPT coordinates of the query heads and of
-// the output), 32 / LPT tokens advance together, and each lane group runs its
-// own softmax state, joined once at the end of a unit.  All arithmetic is
-// fp32.  Masked tokens are not read.
+// Each warp owns 16 tokens of a tile, which lie in one page: LPT lanes share a
+// token (each holds D / LPT coordinates of the query heads and of the output),
+// 32 / LPT tokens advance together, and each lane group runs its own softmax
+// state, joined once at the end of a unit.  All arithmetic is fp32.  A lane
+// copies what it will read of the keys and values a number of steps ahead to
+// shared memory (asynchronously; nobody else reads it, so no barrier is needed),
+// and looks a page up a tile before that: with one step ahead in registers every
+// step waited for DRAM (about 1 us).  Masked tokens are not read.
 template <int D, int GT>
+struct RangeF32 {
+    static constexpr int LPT = GT == 8 ? 16 : 8, TPW = 32 / LPT, E = D / LPT, E4 = E / 4, STEPS = 16 / TPW;
+    static constexpr int AHEAD = E4 == 4 ? 6 : 8;      // steps under way: 32 to 96 KB a CTA
+    static constexpr int SMEM = AHEAD * 2 * E4 * 128 * 16;
+};
+
+template <int D, int GT, bool CLUSTER>
 __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restrict__ k_pool,
-                                                           const float* __restrict__ v_pool, int ps, const RangeArgs a)
+                                                           const float* __restrict__ v_pool, int ps, const RangeArgs a,
+                                                           int cluster)
 {
     pdl_enter();
-    constexpr int LPT = GT == 8 ? 16 : 8, TPW = 32 / LPT, E = D / LPT, E4 = E / 4;
+    using P = RangeF32<D, GT>;
+    constexpr int LPT = P::LPT, TPW = P::TPW, E = P::E, E4 = P::E4, STEPS = P::STEPS, AHEAD = P::AHEAD;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t mine = smem_addr(smem_raw) + threadIdx.x * 16;   // this lane's words, 2 KB apart
     __shared__ float red[4][4][D + kRedPad];
     __shared__ float wm[2][4][4], wl[2][4][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = lane / LPT, sub = lane % LPT;
     const int c_id = blockIdx.x;
-    RangeWalk w = range_start(a, ps, c_id, gridDim.x);
-    if (w.left <= 0) return;
+    const int rank = CLUSTER ? c_id % cluster : 0;
+    __shared__ __align__(16) uint8_t part_raw[CLUSTER ? sizeof(ClusterPart<D>) : 16];
+    ClusterPart<D>& part = *reinterpret_cast<ClusterPart<D>*>(part_raw);
+    RangeWalk w;
+    if (CLUSTER) {
+        w = range_cluster_start(a, ps, c_id / cluster, rank, cluster);
+        if (w.left <= 0 && tid < 8) {
+            part.m[tid] = -INFINITY;
+            part.l[tid] = 0.f;
+        }
+    } else {
+        w = range_start(a, ps, c_id, gridDim.x);
+        if (w.left <= 0) return;
+    }
+    const int b0 = w.b, g0 = w.g;                      // a cluster's unit
     int b = w.b, done = 0, flip = 0;
     while (w.left > 0) {
         const SeqSpan sp = seq_span(a, b, ps, false);
@@ -379,7 +473,7 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
         const int n = (int)min((long long)(nt - w.t), w.left);
         const int u = b * a.H_kv + w.g;
         const bool whole = a.direct && n == nt;
-        if (tid == 0) range_note_span(a, w, u, nt, done, c_id);
+        if (!CLUSTER && tid == 0) range_note_span(a, w, u, nt, done, c_id);
         float q[GT][E], acc[GT][E], mrun[GT], lrun[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
@@ -392,49 +486,89 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
                 acc[h][e] = 0.f;
             }
         }
-        const int steps = 16 / TPW;
-        for (int it = 0; it < n * steps; ++it) {
-            const int tok = warp * 16 + it % steps * TPW + grp;
-            const long long li = ((long long)(w.t + it / steps) * kRangeTile + tok) / ps;
-            const int lp = li < sp.pages() ? sp.logical((int)li) : sp.P;
-            const int pos = lp * ps + tok % ps;
-            bool valid = lp < sp.P && sp.valid(pos);
-            int phys = 0;
-            if (valid) {
-                phys = a.page_table[(size_t)b * a.max_pages + lp];
-                if (phys < 0 || phys >= a.num_phys) {
+        const int last = n * STEPS;
+        // the page of this warp's tokens in the share's tile i (-1 behind the last), and their first position
+        const auto lookup = [&](int i, int& pos) {
+            const long long li = div_ps((long long)(w.t + i) * kRangeTile + warp * 16, ps);
+            if (i >= n || li >= sp.pages()) return -1;
+            const int lp = sp.logical((int)li);
+            pos = lp * ps + ((warp * 16) & (ps - 1));
+            return a.page_table[(size_t)b * a.max_pages + lp];
+        };
+        int pos = 0, pos_next = 0, phys, phys_next = lookup(0, pos_next);
+        uint32_t live = 0;                             // one bit a slot: this lane's token is there
+        int put = 0;
+        const auto fetch = [&](int it) {
+            if (it % STEPS == 0) {
+                phys = phys_next;
+                pos = pos_next;
+                phys_next = lookup(it / STEPS + 1, pos_next);
+                if (phys >= a.num_phys || (phys < 0 && it < last &&
+                                           div_ps((long long)(w.t + it / STEPS) * kRangeTile + warp * 16, ps) < sp.pages())) {
                     report(a.status, ENTMAXKV_DEVICE_BOUNDS);
-                    valid = false;
+                    phys = -1;
                 }
             }
+            const int tok = it % STEPS * TPW + grp;
+            const bool valid = it < last && phys >= 0 && sp.valid(pos + tok);
+            live = valid ? live | (1u << put) : live & ~(1u << put);
+            if (valid) {
+                const size_t row = (((size_t)phys * a.H_kv + w.g) * ps + ((warp * 16) & (ps - 1)) + tok) * D;
+#pragma unroll
+                for (int i = 0; i < E4; ++i) {
+                    const size_t o = row + (i * LPT + sub) * 4;
+                    cp_async16(mine + (put * 2 * E4 + i) * 2048, k_pool + o);
+                    cp_async16(mine + (put * 2 * E4 + E4 + i) * 2048, v_pool + o);
+                }
+            }
+            cp_async_commit();
+            put = put + 1 == AHEAD ? 0 : put + 1;
+        };
+        for (int it = 0; it < AHEAD - 1; ++it) fetch(it);
+        for (int it = 0, get = 0; it < last; ++it, get = get + 1 == AHEAD ? 0 : get + 1) {
+            fetch(it + AHEAD - 1);
+            cp_async_wait<AHEAD - 1>();
+            const bool valid = (live >> get) & 1;
             float4 k4[E4], v4[E4];
-            const size_t row = valid ? (((size_t)phys * a.H_kv + w.g) * ps + tok % ps) * D : 0;
 #pragma unroll
             for (int i = 0; i < E4; ++i) {
-                const size_t o = row + (i * LPT + sub) * 4;
-                k4[i] = valid ? __ldg(reinterpret_cast<const float4*>(k_pool + o)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                v4[i] = valid ? __ldg(reinterpret_cast<const float4*>(v_pool + o)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                k4[i] = valid ? lds128f(mine + (get * 2 * E4 + i) * 2048) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v4[i] = valid ? lds128f(mine + (get * 2 * E4 + E4 + i) * 2048) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             const float* k = reinterpret_cast<const float*>(k4);
             const float* v = reinterpret_cast<const float*>(v4);
+            // the heads side by side: one branch for all, so that their chains overlap
+            float x[GT];
+            bool grow = false;
 #pragma unroll
             for (int h = 0; h < GT; ++h) {
-                float x = 0.f;
+                x[h] = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) x = fmaf(q[h][e], k[e], x);
+                for (int e = 0; e < E; ++e) x[h] = fmaf(q[h][e], k[e], x[h]);
+            }
 #pragma unroll
-                for (int o = LPT / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (!valid) x = -INFINITY;
-                const float mnew = fmaxf(mrun[h], x);
-                const float mu = mnew == -INFINITY ? 0.f : mnew;
-                if (mnew > mrun[h]) {
-                    const float corr = exp2f(mrun[h] - mu);
+            for (int o = LPT / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int h = 0; h < GT; ++h) x[h] += __shfl_xor_sync(0xffffffffu, x[h], o);
+#pragma unroll
+            for (int h = 0; h < GT; ++h) {
+                if (!valid) x[h] = -INFINITY;
+                grow |= x[h] > mrun[h];
+            }
+            if (grow) {
+#pragma unroll
+                for (int h = 0; h < GT; ++h) {
+                    const float mnew = fmaxf(mrun[h], x[h]);
+                    const float corr = mrun[h] == mnew ? 1.f : exp2f(mrun[h] - mnew);
+                    mrun[h] = mnew;
                     lrun[h] *= corr;
 #pragma unroll
                     for (int e = 0; e < E; ++e) acc[h][e] *= corr;
-                    mrun[h] = mnew;
                 }
-                const float p = exp2f(x - mu);
+            }
+#pragma unroll
+            for (int h = 0; h < GT; ++h) {
+                const float p = exp2f(x[h] - (mrun[h] == -INFINITY ? 0.f : mrun[h]));
                 lrun[h] += p;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[h][e] = fmaf(p, v[e], acc[h][e]);
@@ -487,7 +621,15 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
                     const float4 t = *reinterpret_cast<const float4*>(&red[i][h][d]);
                     o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
                 }
-                range_store(a, whole, (long long)c_id + u, b, w.g, 4 * x + h, D, d, o, Mh, L);
+                if (!CLUSTER) {
+                    range_store(a, whole, (long long)c_id + u, b, w.g, 4 * x + h, D, d, o, Mh, L);
+                } else {
+                    *reinterpret_cast<float4*>(&part.o[4 * x + h][d]) = o;
+                    if (d == 0) {
+                        part.m[4 * x + h] = Mh;
+                        part.l[4 * x + h] = L;
+                    }
+                }
             }
         }
         done += n;
@@ -501,6 +643,7 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
             }
         }
     }
+    if (CLUSTER) range_cluster_join<D>(a, part, b0, g0, rank, cluster);
 }
 
 // ---------------------------------------------------------------- merge
@@ -527,40 +670,58 @@ __global__ void __launch_bounds__(kMergeThreads, 4) range_merge_kernel(int ps, c
 }
 
 // ---------------------------------------------------------------- launch
-template <int D, int PS, int NT>
-static int launch_range_bf16(const RangeArgs& a, int C, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                             cudaStream_t stream)
+// `cluster` 0: C CTAs with equal shares; else C CTAs in clusters, one a unit.
+template <typename... KArgs, typename... Args>
+static int launch_range_kernel(void (*kern)(KArgs...), int C, int threads, int cluster, int smem, cudaStream_t stream,
+                               Args&&... args)
 {
-    const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024;
-    if (ensure_smem((const void*)range_bf16_kernel<D, PS, NT>, smem)) return ENTMAXKV_CUDA_ERROR;
-    const cudaError_t e = launch_pdl(range_bf16_kernel<D, PS, NT>, dim3(C), dim3(kRangeThreads), smem, stream, *kmap,
-                                     *vmap, a);
+    if (smem && ensure_smem((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
+    if (cluster > 8 && ensure_cluster_kernel((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
+    const cudaError_t e = cluster ? launch_pdl_cluster(kern, dim3(C), dim3(threads), cluster, smem, stream, args..., cluster)
+                                  : launch_pdl(kern, dim3(C), dim3(threads), smem, stream, args..., cluster);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 
-template <int D>
-static int launch_range_d(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
+template <int D, int PS, bool CLUSTER>
+static int launch_range_bf16(const RangeArgs& a, int C, int cluster, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                             cudaStream_t stream)
+{
+    const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024;
+    return a.G == 8 ? launch_range_kernel(range_bf16_kernel<D, PS, 2, CLUSTER>, C, kRangeThreads, cluster, smem, stream,
+                                          *kmap, *vmap, a)
+                    : launch_range_kernel(range_bf16_kernel<D, PS, 1, CLUSTER>, C, kRangeThreads, cluster, smem, stream,
+                                          *kmap, *vmap, a);
+}
+
+template <int D, bool CLUSTER>
+static int launch_range_d(const entmaxkv_pool& pool, const RangeArgs& a, int C, int cluster, const CUtensorMap* kmap,
                           const CUtensorMap* vmap, cudaStream_t stream)
 {
     if (pool.dtype == ENTMAXKV_F32) {
         const float* k = (const float*)pool.k_pool;
         const float* v = (const float*)pool.v_pool;
-        const cudaError_t e = a.G == 8
-                                  ? launch_pdl(range_f32_kernel<D, 8>, dim3(C), dim3(128), 0, stream, k, v, pool.ps, a)
-                                  : launch_pdl(range_f32_kernel<D, 4>, dim3(C), dim3(128), 0, stream, k, v, pool.ps, a);
-        return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
+        return a.G == 8 ? launch_range_kernel(range_f32_kernel<D, 8, CLUSTER>, C, 128, cluster, RangeF32<D, 8>::SMEM, stream,
+                                              k, v, pool.ps, a)
+                        : launch_range_kernel(range_f32_kernel<D, 4, CLUSTER>, C, 128, cluster, RangeF32<D, 4>::SMEM, stream,
+                                              k, v, pool.ps, a);
     }
-    if (pool.ps == 64) return a.G == 8 ? launch_range_bf16<D, 64, 2>(a, C, kmap, vmap, stream)
-                                       : launch_range_bf16<D, 64, 1>(a, C, kmap, vmap, stream);
-    return a.G == 8 ? launch_range_bf16<D, 16, 2>(a, C, kmap, vmap, stream)
-                    : launch_range_bf16<D, 16, 1>(a, C, kmap, vmap, stream);
+    return pool.ps == 64 ? launch_range_bf16<D, 64, CLUSTER>(a, C, cluster, kmap, vmap, stream)
+                         : launch_range_bf16<D, 16, CLUSTER>(a, C, cluster, kmap, vmap, stream);
 }
 
 int launch_range(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                  const CUtensorMap* vmap, cudaStream_t stream)
 {
-    return pool.d == 128 ? launch_range_d<128>(pool, a, C, kmap, vmap, stream)
-                         : launch_range_d<64>(pool, a, C, kmap, vmap, stream);
+    return pool.d == 128 ? launch_range_d<128, false>(pool, a, C, 0, kmap, vmap, stream)
+                         : launch_range_d<64, false>(pool, a, C, 0, kmap, vmap, stream);
+}
+
+int launch_window_cluster(const entmaxkv_pool& pool, const RangeArgs& a, int cluster, const CUtensorMap* kmap,
+                          const CUtensorMap* vmap, cudaStream_t stream)
+{
+    const int C = a.B * a.H_kv * cluster;
+    return pool.d == 128 ? launch_range_d<128, true>(pool, a, C, cluster, kmap, vmap, stream)
+                         : launch_range_d<64, true>(pool, a, C, cluster, kmap, vmap, stream);
 }
 
 int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
