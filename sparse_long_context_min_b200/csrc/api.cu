@@ -359,15 +359,18 @@ static RangeArgs range_args(const entmaxkv_pool& pool, const float* q, int H_q, 
 // units: a cluster of CTAs each, joined in shared memory, one launch.  Else
 // equal shares of all tiles for two CTAs an SM, and a merge launch.  A cluster
 // has as many CTAs as leave each two tiles, as far as all of them fit the GPU at
-// once; where that leaves a CTA more than 8 tiles, the bytes bound the time and
-// equal shares over all SMs are faster.
+// once; a tile costs a CTA about 0.4 us (fp32 caches: 1.5 us), the merge launch
+// 2 us and more.  Measured, clusters against shares: one sequence of 1028 tokens,
+// 8 kv heads of 128 dims (2 tiles a CTA) 12.1 against 14.3 us; fp32, 24 sequences
+// of up to 2016 tokens, 64 dims (5 tiles) 16.4 against 14.7 us.
 static int launch_ranges(const entmaxkv_pool& pool, const RangeArgs& a, int C, long long pages, const CUtensorMap* kmap,
                          const CUtensorMap* vmap, cudaStream_t stream)
 {
     const long long tiles = (pages * pool.ps + kRangeTile - 1) / kRangeTile, units = (long long)a.B * a.H_kv;
+    const int most = pool.dtype == ENTMAXKV_F32 ? 2 : 6;
     int n = 1;
     while (n < 16 && (tiles + n - 1) / n > 2 && units * 2 * n <= 256) n *= 2;
-    if ((tiles + n - 1) / n <= 8 && units * n <= 256) return launch_window_cluster(pool, a, n, kmap, vmap, stream);
+    if ((tiles + n - 1) / n <= most && units * n <= 256) return launch_window_cluster(pool, a, n, kmap, vmap, stream);
     return launch_window(pool, a, (int)std::min((long long)C, tiles * units), kmap, vmap, stream);
 }
 
