@@ -380,8 +380,8 @@ struct PrefixLayout {
     size_t shared, gid, groups, head, walks, part_o, part_ml, total;
 };
 
-// Rows a unit of the prefix kernel holds, at most.
-constexpr int kPrefixRows = 128;
+// Rows a unit of the prefix kernels holds, at most.
+constexpr int kPrefixRows = 128, kPrefixRowsF32 = 32;
 
 static PrefixLayout prefix_layout(int B, int H_q, int H_kv, int d)
 {
@@ -621,9 +621,9 @@ int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, in
     }
     a.group_start = group_start;
     a.prefix_lens = prefix_lens;
-    a.n_groups = pool->dtype == ENTMAXKV_BF16 ? n_groups : 0;
+    a.n_groups = n_groups;
     a.ps = pool->ps;
-    a.row_tile = kPrefixRows;
+    a.row_tile = pool->dtype == ENTMAXKV_BF16 ? kPrefixRows : kPrefixRowsF32;
     a.block_tok = 64;
     a.C = lay.C;
     a.shared = reinterpret_cast<int32_t*>(ws + lay.shared);

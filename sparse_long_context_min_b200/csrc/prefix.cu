@@ -652,6 +652,270 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
     if (warp == kPfxSoft + 1) tc_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------- fp32 cache
+// The same walk with all arithmetic in fp32: 32 rows and 64 tokens at a time on
+// the ordinary pipes, two products a multiply-add (f32x2).  A producer warp
+// keeps two blocks of keys and of values in shared memory; eight warps share
+// each block: first 8 tokens a warp (a lane: 4 rows x 2 tokens of the scores),
+// then 8 rows of half the tokens a warp (a lane: 4 output dims of 8 rows).
+// Reading shared memory bounds both products: 6 cycles a warp for 32
+// multiply-adds a lane, 3072 cycles a block of 128 dims, against ~2600 in which
+// HBM delivers its 64 KB.
+constexpr int kPfxRowsF32 = 32;
+constexpr int kPfxThreadsF32 = 288;
+
+template <int D>
+struct PfxF32 {
+    static constexpr int KROW = D + 4, PROW = 40;      // padded rows (floats): no two lanes of a read meet in a bank
+    static constexpr int K = 64 * KROW, V = 64 * D, Q = 32 * KROW, P = 64 * PROW;
+    static constexpr int FLOATS = 2 * K + 2 * V + Q + 2 * P;
+};
+
+EKV_DEV void bar_f32() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int D, int PS>
+__global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const float* __restrict__ k_pool,
+                                                                       const float* __restrict__ v_pool,
+                                                                       const PrefixArgs a)
+{
+    pdl_enter();
+    using L = PfxF32<D>;
+    constexpr int KROW = L::KROW, PROW = L::PROW, PPB = 64 / PS, W = D / 32;   // W: output dims of a lane
+    extern __shared__ __align__(128) float sm[];
+    float* ks = sm;                                    // [2][64][KROW]
+    float* vs = ks + 2 * L::K;                         // [2][64][D]
+    float* qs = vs + 2 * L::V;                         // [32][KROW]; then the second token half's output
+    float* ps = qs + L::Q;                             // [2][64][PROW]
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    __shared__ int top_of[32];                         // largest score so far, as an ordered integer
+    __shared__ float lsum[8][32];
+    __shared__ volatile int dead;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t* status = a.r.status;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&k_empty[i], 8);
+            mbar_init(&v_empty[i], 8);
+        }
+        fence_mbar_init();
+        dead = 0;
+    }
+    __syncthreads();
+    PrefixWalk w = a.walks[blockIdx.x];
+    int k0, n;
+    if (warp == 8) {
+        // ---------------------------------------------------- producer
+        int it = 0;
+        bool go = true;
+        for (; go && prefix_segment(a, w, k0, n); prefix_advance(a, w)) {
+            const PrefixGroup& G = a.groups[w.j];
+            const int32_t* pages = a.r.page_table + (size_t)G.first * a.r.max_pages;
+            for (int i = 0; i < n && go; ++i, ++it) {
+                // a token's page; pages past the shared ones repeat the block's first (their scores are masked,
+                // and the weight of zero must meet a value that some row uses anyway)
+                int ph = -1;
+                if (lane < PPB) {
+                    int p = (k0 + i) * PPB + lane;
+                    if (p >= G.pages) p = (k0 + i) * PPB;
+                    ph = pages[p];
+                    if (ph < 0 || ph >= a.r.num_phys) {
+                        report(status, ENTMAXKV_DEVICE_BOUNDS);
+                        ph = -1;
+                    }
+                }
+                const int slot = it & 1;
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ph >= 0)) * PS * D * 4;
+                if (it >= 2) go = pfx_wait(&k_empty[slot], ((it >> 1) - 1) & 1, &dead, status);
+                if (!go) break;
+                if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], bytes);
+                __syncwarp();
+                for (int t = lane; t < 64; t += 32) {
+                    const int phys = __shfl_sync(0xffffffffu, ph, t / PS);
+                    if (phys >= 0)
+                        bulk_load(ks + slot * L::K + t * KROW,
+                                  k_pool + (((size_t)phys * a.r.H_kv + w.g) * PS + t % PS) * D, D * 4, &k_full[slot]);
+                }
+                if (it >= 2) go = pfx_wait(&v_empty[slot], ((it >> 1) - 1) & 1, &dead, status);
+                if (!go) {                             // the keys on their way must land
+                    if (lane == 0) mbar_wait(&k_full[slot], (it >> 1) & 1, kWaitLimitNs);
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&v_full[slot], bytes);
+                __syncwarp();
+                if (ph >= 0)
+                    bulk_load(vs + slot * L::V + lane * PS * D, v_pool + ((size_t)ph * a.r.H_kv + w.g) * PS * D,
+                              PS * D * 4, &v_full[slot]);
+            }
+        }
+        if (!go && lane == 0)                          // and so must the blocks before
+            for (int i = max(0, it - 2); i < it; ++i) {
+                mbar_wait(&k_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+                mbar_wait(&v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+            }
+        return;
+    }
+    // -------------------------------------------------------- consumers
+    const int rg = lane & 7, tg = lane >> 3;           // scores: rows rg + 8 j, tokens 8 warp + tg + 4 i
+    const int half = warp >> 2, r8 = (warp & 3) * 8;   // outputs: rows r8 .. r8 + 7, tokens of one half
+    const int lg = __ffs(a.r.G) - 1;
+    int it = 0;
+    for (; prefix_segment(a, w, k0, n); prefix_advance(a, w)) {
+        const PrefixGroup& G = a.groups[w.j];
+        const int rows = min(kPfxRowsF32, G.rows - w.t * kPfxRowsF32);
+        for (int i = tid; i < 32 * D / 4; i += 256) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4, r = w.t * kPfxRowsF32 + row;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows) {
+                x = *reinterpret_cast<const float4*>(
+                    a.r.q + ((size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1))) * D + d);
+                x.x *= a.r.xscale; x.y *= a.r.xscale; x.z *= a.r.xscale; x.w *= a.r.xscale;
+            }
+            *reinterpret_cast<float4*>(qs + row * KROW + d) = x;
+        }
+        if (tid < 32) top_of[tid] = ordered_int(-INFINITY);
+        float m[4], l[4], mo[8], acc[8][W];            // maxima of the score rows and of the output rows
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = -INFINITY;
+            l[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            mo[j] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < W; ++e) acc[j][e] = 0.f;
+        }
+        bar_f32();
+        for (int i = 0; i < n; ++i, ++it) {
+            const int slot = it & 1;
+            float* pb = ps + slot * L::P;
+            if (pfx_wait(&k_full[slot], (it >> 1) & 1, &dead, status)) {
+                uint64_t s[4][2] = {};
+                const float* kr = ks + slot * L::K + (warp * 8 + tg) * KROW;
+                const float* qr = qs + rg * KROW;
+#pragma unroll 4
+                for (int d = 0; d < D; d += 4) {
+                    ulonglong2 kv[2], qv[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) kv[e] = *reinterpret_cast<const ulonglong2*>(kr + e * 4 * KROW + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) qv[j] = *reinterpret_cast<const ulonglong2*>(qr + j * 8 * KROW + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            s[j][e] = fma2(qv[j].x, kv[e].x, s[j][e]);
+                            s[j][e] = fma2(qv[j].y, kv[e].y, s[j][e]);
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_empty[slot]);
+                const long long left = (long long)G.pages * PS - (long long)(k0 + i) * 64;
+                float x[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 t = unpair(s[j][e]);
+                        x[j][e] = warp * 8 + tg + 4 * e < left ? t.x + t.y : -INFINITY;
+                    }
+                    float top = fmaxf(x[j][0], x[j][1]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    if (tg == 0) atomicMax(&top_of[rg + 8 * j], ordered_int(top));
+                }
+                bar_f32();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float mn = ordered_float(*(volatile int*)&top_of[rg + 8 * j]);
+                    const float mu = mn == -INFINITY ? 0.f : mn;
+                    l[j] *= m[j] == -INFINITY ? 0.f : exp2f(m[j] - mn);
+                    m[j] = mn;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float p = exp2f(x[j][e] - mu);
+                        l[j] += p;
+                        pb[(warp * 8 + tg + 4 * e) * PROW + rg + 8 * j] = p;
+                    }
+                }
+            } else {
+                bar_f32();
+            }
+            float f[8];
+            bool grow = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float mn = ordered_float(*(volatile int*)&top_of[r8 + j]);
+                f[j] = mo[j] == mn ? 1.f : mo[j] == -INFINITY ? 0.f : exp2f(mo[j] - mn);
+                grow |= mo[j] != mn;
+                mo[j] = mn;
+            }
+            bar_f32();                                 // weights written, maxima read
+            if (grow)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[j][e] *= f[j];
+            if (pfx_wait(&v_full[slot], (it >> 1) & 1, &dead, status)) {
+                const float* vr = vs + slot * L::V + half * 32 * D + lane * W;
+                const float* pr = pb + half * 32 * PROW + r8;
+#pragma unroll 4
+                for (int t = 0; t < 32; ++t) {
+                    const float4 p0 = *reinterpret_cast<const float4*>(pr + t * PROW);
+                    const float4 p1 = *reinterpret_cast<const float4*>(pr + t * PROW + 4);
+                    const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+                    uint64_t v[W / 2];
+#pragma unroll
+                    for (int e = 0; e < W / 2; ++e) v[e] = *reinterpret_cast<const uint64_t*>(vr + t * D + 2 * e);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < W / 2; ++e) {
+                            const float2 o = unpair(fma2(pair(p[j], p[j]), v[e], pair(acc[j][2 * e], acc[j][2 * e + 1])));
+                            acc[j][2 * e] = o.x;
+                            acc[j][2 * e + 1] = o.y;
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_empty[slot]);
+            }
+        }
+        // join the token halves and the rows' sums
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+            if (tg == 0) lsum[warp][rg + 8 * j] = l[j];
+        }
+        bar_f32();                                     // also: Q is not read any more
+        if (half == 1)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < W; ++e) qs[(r8 + j) * KROW + lane * W + e] = acc[j][e];
+        bar_f32();
+        const long long part_row = prefix_part_row(a, G, w.g, w.t, blockIdx.x);
+        if (half == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r8 + j < rows)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        const int d = lane * W + e;
+                        a.part_o[part_row * D + ((long long)(d / 4) * rows + r8 + j) * 4 + d % 4] =
+                            acc[j][e] + qs[(r8 + j) * KROW + d];
+                    }
+        if (tid < rows) {
+            float sum = 0.f;
+            for (int i = 0; i < 8; ++i) sum += lsum[i][tid];
+            reinterpret_cast<float2*>(a.part_ml)[part_row + tid] = make_float2(ordered_float(top_of[tid]), sum);
+        }
+        bar_f32();                                     // Q, sums and maxima may come again
+    }
+}
+
 // ---------------------------------------------------------------- merge
 // One CTA a (sequence, kv head): the prefix partials in CTA order, then its own.
 constexpr int kPrefixMergeThreads = 256;
@@ -708,6 +972,17 @@ static int launch_prefix_bf16(const PrefixArgs& a, const CUtensorMap* kmap, cons
                : ENTMAXKV_CUDA_ERROR;
 }
 
+template <int D, int PS>
+static int launch_prefix_f32(const entmaxkv_pool& pool, const PrefixArgs& a, cudaStream_t stream)
+{
+    const int smem = PfxF32<D>::FLOATS * 4;
+    if (ensure_smem((const void*)prefix_f32_kernel<D, PS>, smem)) return ENTMAXKV_CUDA_ERROR;
+    return launch_pdl(prefix_f32_kernel<D, PS>, dim3(a.C), dim3(kPfxThreadsF32), smem, stream, (const float*)pool.k_pool,
+                      (const float*)pool.v_pool, a) == cudaSuccess
+               ? ENTMAXKV_OK
+               : ENTMAXKV_CUDA_ERROR;
+}
+
 int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream)
 {
@@ -721,6 +996,10 @@ int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, c
         else
             rc = pool.ps == 64 ? launch_prefix_bf16<64, 64>(a, kmap, vmap, stream)
                                : launch_prefix_bf16<64, 16>(a, kmap, vmap, stream);
+    } else if (pool.d == 128) {
+        rc = pool.ps == 64 ? launch_prefix_f32<128, 64>(pool, a, stream) : launch_prefix_f32<128, 16>(pool, a, stream);
+    } else {
+        rc = pool.ps == 64 ? launch_prefix_f32<64, 64>(pool, a, stream) : launch_prefix_f32<64, 16>(pool, a, stream);
     }
     if (rc) return rc;
     if ((rc = launch_range(pool, a.r, range_C, kmap, vmap, stream))) return rc;

@@ -93,8 +93,9 @@ def test_groups_of_every_kind(H_q, H_kv, d, ps, dtype):
     c.verify()
 
 
-def test_long_prefix_is_cut_between_ctas():
-    c = Shared([(9000, [9000 + 13 * i for i in range(3)]), (5000, [5001] * 37)], 16, 2, 128, 64, BF16, seed=11)
+@pytest.mark.parametrize("d,ps,dtype", [(128, 64, BF16), (64, 16, BF16), (128, 16, F32), (64, 64, F32)])
+def test_long_prefix_is_cut_between_ctas(d, ps, dtype):
+    c = Shared([(9000, [9000 + 13 * i for i in range(3)]), (5000, [5001] * 37)], 16, 2, d, ps, dtype, seed=11)
     c.verify()
 
 
