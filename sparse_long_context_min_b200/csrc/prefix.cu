@@ -654,21 +654,23 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
 
 // ---------------------------------------------------------------- fp32 cache
 // The same walk with all arithmetic in fp32: 32 rows and 64 tokens at a time on
-// the ordinary pipes, two products a multiply-add (f32x2).  A producer warp
-// keeps two blocks of keys and of values in shared memory; eight warps share
-// each block: first 8 tokens a warp (a lane: 4 rows x 2 tokens of the scores),
-// then 8 rows of half the tokens a warp (a lane: 4 output dims of 8 rows).
-// Reading shared memory bounds both products: 6 cycles a warp for 32
-// multiply-adds a lane, 3072 cycles a block of 128 dims, against ~2600 in which
-// HBM delivers its 64 KB.
+// the ordinary pipes, two multiply-adds an instruction (f32x2).  A producer warp
+// keeps two blocks of keys and of values in shared memory; each of eight warps
+// has 8 rows and 32 tokens of every block to itself, scores (a lane a token) and
+// output (a lane D / 32 dims), with its own softmax state, so that no barrier
+// stands between the blocks; the token halves are joined at a unit's end.
+// Reading shared memory bounds it (its pipe is 77% busy at 64 rows): 20 cycles a
+// warp for 32 multiply-adds a lane of the scores, 8 of the output, 7200 cycles a
+// block of 32 rows and 128 dims against ~2600 in which HBM delivers its 64 KB;
+// warps without rows stay out of the way.
 constexpr int kPfxRowsF32 = 32;
 constexpr int kPfxThreadsF32 = 288;
 
 template <int D>
 struct PfxF32 {
-    static constexpr int KROW = D + 4, PROW = 40;      // padded rows (floats): no two lanes of a read meet in a bank
-    static constexpr int K = 64 * KROW, V = 64 * D, Q = 32 * KROW, P = 64 * PROW;
-    static constexpr int FLOATS = 2 * K + 2 * V + Q + 2 * P;
+    static constexpr int KROW = D + 4, PROW = 12;      // padded rows (floats): no two lanes of a read meet in a bank
+    static constexpr int K = 64 * KROW, V = 64 * D, Q = 32 * KROW, P = 8 * 32 * PROW;
+    static constexpr int FLOATS = 2 * K + 2 * V + Q + P;
 };
 
 EKV_DEV void bar_f32() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -685,10 +687,9 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
     float* ks = sm;                                    // [2][64][KROW]
     float* vs = ks + 2 * L::K;                         // [2][64][D]
     float* qs = vs + 2 * L::V;                         // [32][KROW]; then the second token half's output
-    float* ps = qs + L::Q;                             // [2][64][PROW]
+    float* ps = qs + L::Q;                             // [8 warps][32 tokens][PROW]
     __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    __shared__ int top_of[32];                         // largest score so far, as an ordered integer
-    __shared__ float lsum[8][32];
+    __shared__ float2 ml[32];                          // the second token half's maxima and sums
     __shared__ volatile int dead;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t* status = a.r.status;
@@ -757,8 +758,8 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
         return;
     }
     // -------------------------------------------------------- consumers
-    const int rg = lane & 7, tg = lane >> 3;           // scores: rows rg + 8 j, tokens 8 warp + tg + 4 i
-    const int half = warp >> 2, r8 = (warp & 3) * 8;   // outputs: rows r8 .. r8 + 7, tokens of one half
+    const int half = warp >> 2, r8 = (warp & 3) * 8;
+    float* pw = ps + warp * 32 * PROW;
     const int lg = __ffs(a.r.G) - 1;
     int it = 0;
     for (; prefix_segment(a, w, k0, n); prefix_advance(a, w)) {
@@ -774,154 +775,117 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
             }
             *reinterpret_cast<float4*>(qs + row * KROW + d) = x;
         }
-        if (tid < 32) top_of[tid] = ordered_int(-INFINITY);
-        float m[4], l[4], mo[8], acc[8][W];            // maxima of the score rows and of the output rows
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = -INFINITY;
-            l[j] = 0.f;
-        }
+        float m[8], l[8], acc[8][W];                   // m: the same in all lanes; l: of this lane's tokens
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            mo[j] = -INFINITY;
+            m[j] = -INFINITY;
+            l[j] = 0.f;
 #pragma unroll
             for (int e = 0; e < W; ++e) acc[j][e] = 0.f;
         }
         bar_f32();
         for (int i = 0; i < n; ++i, ++it) {
             const int slot = it & 1;
-            float* pb = ps + slot * L::P;
-            if (pfx_wait(&k_full[slot], (it >> 1) & 1, &dead, status)) {
-                uint64_t s[4][2] = {};
-                const float* kr = ks + slot * L::K + (warp * 8 + tg) * KROW;
-                const float* qr = qs + rg * KROW;
-#pragma unroll 4
-                for (int d = 0; d < D; d += 4) {
-                    ulonglong2 kv[2], qv[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) kv[e] = *reinterpret_cast<const ulonglong2*>(kr + e * 4 * KROW + d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) qv[j] = *reinterpret_cast<const ulonglong2*>(qr + j * 8 * KROW + d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            s[j][e] = fma2(qv[j].x, kv[e].x, s[j][e]);
-                            s[j][e] = fma2(qv[j].y, kv[e].y, s[j][e]);
-                        }
-                }
-                __syncwarp();
+            if (!pfx_wait(&k_full[slot], (it >> 1) & 1, &dead, status)) continue;
+            if (r8 >= rows) {
                 if (lane == 0) mbar_arrive(&k_empty[slot]);
-                const long long left = (long long)G.pages * PS - (long long)(k0 + i) * 64;
-                float x[4][2];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 t = unpair(s[j][e]);
-                        x[j][e] = warp * 8 + tg + 4 * e < left ? t.x + t.y : -INFINITY;
-                    }
-                    float top = fmaxf(x[j][0], x[j][1]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    if (tg == 0) atomicMax(&top_of[rg + 8 * j], ordered_int(top));
-                }
-                bar_f32();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float mn = ordered_float(*(volatile int*)&top_of[rg + 8 * j]);
-                    const float mu = mn == -INFINITY ? 0.f : mn;
-                    l[j] *= m[j] == -INFINITY ? 0.f : exp2f(m[j] - mn);
-                    m[j] = mn;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p = exp2f(x[j][e] - mu);
-                        l[j] += p;
-                        pb[(warp * 8 + tg + 4 * e) * PROW + rg + 8 * j] = p;
-                    }
-                }
-            } else {
-                bar_f32();
+                if (pfx_wait(&v_full[slot], (it >> 1) & 1, &dead, status) && lane == 0) mbar_arrive(&v_empty[slot]);
+                continue;
             }
-            float f[8];
-            bool grow = false;
+            uint64_t s[8] = {};
+            const float* kr = ks + slot * L::K + (half * 32 + lane) * KROW;
+            const float* qr = qs + r8 * KROW;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kr + d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qr + j * KROW + d);
+                    s[j] = fma2(q.x, k.x, s[j]);
+                    s[j] = fma2(q.y, k.y, s[j]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_empty[slot]);
+            const bool valid = half * 32 + lane < (long long)G.pages * PS - (long long)(k0 + i) * 64;
+            float p[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float mn = ordered_float(*(volatile int*)&top_of[r8 + j]);
-                f[j] = mo[j] == mn ? 1.f : mo[j] == -INFINITY ? 0.f : exp2f(mo[j] - mn);
-                grow |= mo[j] != mn;
-                mo[j] = mn;
+                const float2 t = unpair(s[j]);
+                p[j] = valid ? t.x + t.y : -INFINITY;
+                const float mn = fmaxf(m[j], ordered_float(__reduce_max_sync(0xffffffffu, ordered_int(p[j]))));
+                if (mn != m[j]) {                      // all lanes alike
+                    const float f = m[j] == -INFINITY ? 0.f : exp2f(m[j] - mn);
+                    m[j] = mn;
+                    l[j] *= f;
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[j][e] *= f;
+                }
+                p[j] = exp2f(p[j] - (mn == -INFINITY ? 0.f : mn));
+                l[j] += p[j];
             }
-            bar_f32();                                 // weights written, maxima read
-            if (grow)
+            reinterpret_cast<float4*>(pw + lane * PROW)[0] = make_float4(p[0], p[1], p[2], p[3]);
+            reinterpret_cast<float4*>(pw + lane * PROW)[1] = make_float4(p[4], p[5], p[6], p[7]);
+            __syncwarp();
+            if (!pfx_wait(&v_full[slot], (it >> 1) & 1, &dead, status)) continue;
+            const float* vr = vs + slot * L::V + half * 32 * D + lane * W;
+#pragma unroll 4
+            for (int t = 0; t < 32; ++t) {
+                const float4 p0 = *reinterpret_cast<const float4*>(pw + t * PROW);
+                const float4 p1 = *reinterpret_cast<const float4*>(pw + t * PROW + 4);
+                const float pt[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+                float v[W];
+                if constexpr (W == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(vr + t * D);
+                else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vr + t * D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
-                    for (int e = 0; e < W; ++e) acc[j][e] *= f[j];
-            if (pfx_wait(&v_full[slot], (it >> 1) & 1, &dead, status)) {
-                const float* vr = vs + slot * L::V + half * 32 * D + lane * W;
-                const float* pr = pb + half * 32 * PROW + r8;
-#pragma unroll 4
-                for (int t = 0; t < 32; ++t) {
-                    const float4 p0 = *reinterpret_cast<const float4*>(pr + t * PROW);
-                    const float4 p1 = *reinterpret_cast<const float4*>(pr + t * PROW + 4);
-                    const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-                    uint64_t v[W / 2];
-#pragma unroll
-                    for (int e = 0; e < W / 2; ++e) v[e] = *reinterpret_cast<const uint64_t*>(vr + t * D + 2 * e);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < W / 2; ++e) {
-                            const float2 o = unpair(fma2(pair(p[j], p[j]), v[e], pair(acc[j][2 * e], acc[j][2 * e + 1])));
-                            acc[j][2 * e] = o.x;
-                            acc[j][2 * e + 1] = o.y;
-                        }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&v_empty[slot]);
+                    for (int e = 0; e < W; e += 2) {
+                        const float2 o = unpair(fma2(pair(pt[j], pt[j]), pair(v[e], v[e + 1]), pair(acc[j][e], acc[j][e + 1])));
+                        acc[j][e] = o.x;
+                        acc[j][e + 1] = o.y;
+                    }
             }
+            __syncwarp();                              // also: the weights have been read
+            if (lane == 0) mbar_arrive(&v_empty[slot]);
         }
-        // join the token halves and the rows' sums
+        // join the token halves
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
-            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
-            if (tg == 0) lsum[warp][rg + 8 * j] = l[j];
-        }
-        bar_f32();                                     // also: Q is not read any more
+        for (int j = 0; j < 8; ++j) l[j] = warp_sum(l[j]);
+        bar_f32();                                     // Q is not read any more
         if (half == 1)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j) {
+                if (lane == 0) ml[r8 + j] = make_float2(m[j], l[j]);
 #pragma unroll
                 for (int e = 0; e < W; ++e) qs[(r8 + j) * KROW + lane * W + e] = acc[j][e];
+            }
         bar_f32();
         const long long part_row = prefix_part_row(a, G, w.g, w.t, blockIdx.x);
         if (half == 0)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (r8 + j < rows)
+                if (r8 + j < rows) {
+                    const float2 x = ml[r8 + j];
+                    const float M = fmaxf(m[j], x.x);
+                    const float f0 = m[j] == -INFINITY ? 0.f : exp2f(m[j] - M), f1 = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
                         const int d = lane * W + e;
                         a.part_o[part_row * D + ((long long)(d / 4) * rows + r8 + j) * 4 + d % 4] =
-                            acc[j][e] + qs[(r8 + j) * KROW + d];
+                            acc[j][e] * f0 + qs[(r8 + j) * KROW + d] * f1;
                     }
-        if (tid < rows) {
-            float sum = 0.f;
-            for (int i = 0; i < 8; ++i) sum += lsum[i][tid];
-            reinterpret_cast<float2*>(a.part_ml)[part_row + tid] = make_float2(ordered_float(top_of[tid]), sum);
-        }
-        bar_f32();                                     // Q, sums and maxima may come again
+                    if (lane == 0)
+                        reinterpret_cast<float2*>(a.part_ml)[part_row + r8 + j] = make_float2(M, l[j] * f0 + x.y * f1);
+                }
+        bar_f32();                                     // Q may come again
     }
 }
 
 // ---------------------------------------------------------------- merge
 // One CTA a (sequence, kv head): the prefix partials in CTA order, then its own.
-constexpr int kPrefixMergeThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kPrefixMergeThreads, 4) prefix_merge_kernel(const PrefixArgs a)
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) prefix_merge_kernel(const PrefixArgs a)
 {
     pdl_enter();
     const RangeArgs& r = a.r;
@@ -948,7 +912,7 @@ __global__ void __launch_bounds__(kPrefixMergeThreads, 4) prefix_merge_kernel(co
     }
     float4 o;
     float m, l;
-    if (!merge_parts<D, kPrefixMergeThreads>(list[0], list[1], r.G, o, m, l)) return;
+    if (!merge_parts<D, THREADS>(list[0], list[1], r.G, o, m, l)) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const size_t row = (size_t)b * r.H_q + (size_t)g * r.G + h;
     float* dst = r.out + row * D + d4 * 4;
@@ -1003,10 +967,12 @@ int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, c
     }
     if (rc) return rc;
     if ((rc = launch_range(pool, a.r, range_C, kmap, vmap, stream))) return rc;
-    const dim3 grid(a.r.B * a.r.H_kv);
-    const cudaError_t e = pool.d == 128 ? launch_pdl(prefix_merge_kernel<128>, grid, dim3(kPrefixMergeThreads), 0, stream, a)
-                                        : launch_pdl(prefix_merge_kernel<64>, grid, dim3(kPrefixMergeThreads), 0, stream, a);
-    return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
+    const int n = a.r.B * a.r.H_kv;
+    const auto merge = merge_threads(n) == 1024
+                           ? (pool.d == 128 ? prefix_merge_kernel<128, 1024> : prefix_merge_kernel<64, 1024>)
+                           : (pool.d == 128 ? prefix_merge_kernel<128, 256> : prefix_merge_kernel<64, 256>);
+    return launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, a) == cudaSuccess ? ENTMAXKV_OK
+                                                                                          : ENTMAXKV_CUDA_ERROR;
 }
 
 }  // namespace ekv

@@ -649,10 +649,8 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
 // ---------------------------------------------------------------- merge
 // One CTA a unit: rows of a unit that several CTAs share are joined; rows of a
 // unit without tokens get o = 0 and lse = -infinity.
-constexpr int kMergeThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 4) range_merge_kernel(int ps, const RangeArgs a)
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) range_merge_kernel(int ps, const RangeArgs a)
 {
     pdl_enter();
     const int u = blockIdx.x, b = u / a.H_kv, g = u % a.H_kv;
@@ -666,7 +664,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) range_merge_kernel(int ps, c
                         empty ? 0 : sp.y - sp.x + 1};
     float4 o;
     float m, l;
-    if (merge_parts<D, kMergeThreads>(list, PartList{}, a.G, o, m, l)) range_store(a, true, 0, b, g, h, D, d, o, m, l);
+    if (merge_parts<D, THREADS>(list, PartList{}, a.G, o, m, l)) range_store(a, true, 0, b, g, h, D, d, o, m, l);
 }
 
 // ---------------------------------------------------------------- launch
@@ -729,11 +727,12 @@ int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CU
 {
     const int rc = launch_range(pool, a, C, kmap, vmap, stream);
     if (rc) return rc;
-    const dim3 grid(a.B * a.H_kv);
-    const cudaError_t e = pool.d == 128
-                              ? launch_pdl(range_merge_kernel<128>, grid, dim3(kMergeThreads), 0, stream, pool.ps, a)
-                              : launch_pdl(range_merge_kernel<64>, grid, dim3(kMergeThreads), 0, stream, pool.ps, a);
-    return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
+    const int n = a.B * a.H_kv;
+    const auto merge = merge_threads(n) == 1024
+                           ? (pool.d == 128 ? range_merge_kernel<128, 1024> : range_merge_kernel<64, 1024>)
+                           : (pool.d == 128 ? range_merge_kernel<128, 256> : range_merge_kernel<64, 256>);
+    return launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, pool.ps, a) == cudaSuccess ? ENTMAXKV_OK
+                                                                                                   : ENTMAXKV_CUDA_ERROR;
 }
 
 }  // namespace ekv
