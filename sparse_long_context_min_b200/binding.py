@@ -123,11 +123,12 @@ class _Args:
 
     def pool(self, pool):
         """The pool's memory belongs to the device that was current when it was made."""
-        if pool.index >= 0:
+        index = pool.k_pool.get_device()
+        if index >= 0:
             if self.dev is None:
                 self.dev = torch.cuda.current_device()
-            if pool.index != self.dev:
-                self.fail("the pool is on cuda:%d, the current device is cuda:%d" % (pool.index, self.dev))
+            if index != self.dev:
+                self.fail("the pool is on cuda:%d, the current device is cuda:%d" % (index, self.dev))
 
     def need(self, t, name, dtype=None, numel=0, dims=None):
         if t is None:
@@ -205,7 +206,6 @@ class Pool:
                         mean.data_ptr(), m2.data_ptr(), count.data_ptr(), self.num_phys, self.H_kv,
                         self.ps, self.d, self.dtype)
         self.c = ctypes.byref(self._c)
-        self.index = k_pool.get_device()
 
     @classmethod
     def allocate(cls, num_phys, H_kv, ps, d, dtype=torch.bfloat16, device="cuda"):

@@ -725,6 +725,7 @@ int launch_fork(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table, in
                p.head, p.free_ids, p.want, p.at, status};
     const PageBytes pb = page_bytes(pool);
     const int row_chunks = (max_pages + kRowChunk - 1) / kRowChunk;
+    if ((long long)n * (row_chunks + pb.chunks) > INT32_MAX) return ENTMAXKV_UNSUPPORTED;
     int rc = done(launch_pdl(fork_release_kernel, dim3(n, row_chunks), dim3(kRowThreads), 0, stream, f));
     if (rc) return rc;
     if ((rc = launch_plan<false>(p, stream))) return rc;

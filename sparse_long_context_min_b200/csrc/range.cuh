@@ -229,7 +229,7 @@ EKV_DEV bool merge_parts(const PartList& x, const PartList& y, int G, float4& o,
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto join = [&](float4 t, float2 ml) {
-        if (ml.x == -INFINITY) return;
+        if (ml.y == 0.f) return;                       // no tokens (a sum that is NaN goes on)
         const float mn = fmaxf(m, ml.x);
         const float f = exp2f(m - mn), e = exp2f(ml.x - mn);
         m = mn;

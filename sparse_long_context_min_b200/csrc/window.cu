@@ -92,7 +92,7 @@ EKV_DEV void range_cluster_join(const RangeArgs& a, ClusterPart<D>& part, int b,
                 }
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (c0 + k < n && m[k] != -INFINITY) {
+                if (c0 + k < n && s[k] != 0.f) {
                     const float mn = fmaxf(M, m[k]);
                     const float f = exp2f(M - mn), e = exp2f(m[k] - mn);
                     M = mn;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float mi = wm[flip][i][h];
-                    if (mi != -INFINITY) L += wl[flip][i][h] * exp2f(mi - Mh);
+                    L += wl[flip][i][h] * (mi == -INFINITY ? 0.f : exp2f(mi - Mh));   // (a sum that is NaN stays)
                     const float4 t = *reinterpret_cast<const float4*>(red + (i * 4 + h) * RED + d);
                     o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
                 }
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int i = 0; i < 4; ++i) {
                     const float mi = wm[flip][i][h];
-                    if (mi != -INFINITY) L += wl[flip][i][h] * exp2f(mi - Mh);
+                    L += wl[flip][i][h] * (mi == -INFINITY ? 0.f : exp2f(mi - Mh));   // (a sum that is NaN stays)
                     const float4 t = *reinterpret_cast<const float4*>(&red[i][h][d]);
                     o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
                 }
