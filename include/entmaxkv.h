@@ -356,6 +356,9 @@ ENTMAXKV_API int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const
  *   0 <= n_groups <= B (0: group_start and prefix_lens may be NULL).
  *   A sequence without tokens gets out = 0 and lse = -INFINITY.  The same call
  *   gives the same bits.
+ *   Small calls (B * max_pages pages of keys and values under 64 MiB) and calls
+ *   whose q is not 16-byte aligned read the prefix for each sequence: two launches
+ *   instead of four take less time than such prefixes do.
  *   workspace: entmaxkv_workspace_size(ENTMAXKV_OP_PREFIX_SOFTMAX, ...) bytes
  *   (k_max ignored).
  */
@@ -412,6 +415,7 @@ ENTMAXKV_API int entmaxkv_copy_pages(const entmaxkv_pool* pool, const int32_t* s
  *   any pair's source is refused: skipped and reported, its rows as they were.
  *   When the pool runs out of pages the forks served last are left empty
  *   (length 0, no pages) and ENTMAXKV_NO_PAGES is reported.
+ *   ENTMAXKV_UNSUPPORTED when n times a page's 16 KB pieces pass 31 bits.
  */
 ENTMAXKV_API int entmaxkv_fork_sequences(const entmaxkv_pool* pool, int32_t* ref, int32_t* page_table,
                             int32_t max_pages, int32_t* seq_lens, int32_t B, const int32_t* src,

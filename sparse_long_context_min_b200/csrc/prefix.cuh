@@ -49,7 +49,7 @@ struct PrefixArgs {
 // To start a unit costs a CTA about as long as kPrefixTurn blocks (its query,
 // the end of the pipeline before, its results): every unit is laid out with as
 // many blocks in front that hold no work.
-constexpr int kPrefixTurn = 4;
+constexpr int kPrefixTurn = 6;
 
 EKV_DEV int prefix_len(const PrefixGroup& G) { return G.blocks + kPrefixTurn; }
 

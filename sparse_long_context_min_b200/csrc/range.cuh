@@ -208,11 +208,11 @@ struct PartList {
     int n;
 };
 
-// Threads of a merge CTA.  Few rows have many partials each (up to a CTA's worth),
-// and CTAs to spare; many rows have few.  Measured (the merge alone, profiled): 32
+// Threads of a merge CTA.  Few rows have many partials each (up to a CTA's worth)
+// and SMs to spare; many rows have few.  Measured (the merge alone, profiled): 32
 // CTAs of 75 partials 15.2 us with 256 threads, 10.0 with 1024; 768 CTAs of 8
 // partials 11 us with 256, 16 with 512.
-inline int merge_threads(int ctas) { return ctas <= 2 * num_sms() ? 1024 : 256; }
+inline int merge_threads(int ctas) { return ctas <= num_sms() ? 1024 : 256; }
 
 // Joins the partials of list x, then those of list y, of G rows of D dims: the
 // block's threads form teams of G * D / 4 (one float4 of one row a thread),
