@@ -171,6 +171,33 @@ def test_large_pool_and_long_rows():
     s.copy(ids[:1500], ids[1500:])
 
 
+def test_wide_tables():
+    """More entries than the counting cluster takes along: releasing and counting are launches of their own."""
+    s = Both(3000, 3, 17000, 16, 1, 64)
+    s.reserve([20000, 0, 33])
+    s.set_lens([20000, 0, 33])
+    s.fork([0, 0], [1, 2])
+    s.set_lens([20000, 20000, 19999])
+    s.fork([2, 2], [0, 1])
+    s.fork([0, 2], [0, 1])                    # a destination that is a source
+    s.reserve([17000 * 16 + 1, 24000, 24001])
+    s.reserve([0, 39000, 47000])              # more than there are
+    s.free([0, 2])
+    s.compact()
+
+
+def test_many_forks_of_short_rows():
+    """More forks than warps of the counting cluster, some refused."""
+    rows = 700
+    s = Both(1500, rows, 4)
+    s.reserve([37 if b < 300 else 0 for b in range(rows)])
+    s.set_lens([37 if b < 300 else 0 for b in range(rows)])
+    rng = random.Random(8)
+    dst = rng.sample(range(300, rows), 290)
+    s.fork([rng.randrange(300) for _ in dst] + [5], dst + [dst[0]])
+    s.fork([rng.randrange(300) for _ in range(40)], rng.sample(range(300, rows), 40))
+
+
 def test_nothing_to_do():
     s = Both(8, 2, 4)
     s.compact()
