@@ -41,10 +41,10 @@ struct RangeArgs {
     int direct;                    // write finished units straight to out
 };
 
-// The kernels over each sequence's range (window.cu), C CTAs.
+// The kernels over each sequence's tokens behind a shared prefix (window.cu), C CTAs.
 int launch_range(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                  const CUtensorMap* vmap, cudaStream_t stream);
-// The same, and the merge of units that CTAs share.
+// The kernels over windows, and the merge of units that CTAs share.
 int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream);
 // The same as one launch, a cluster of `cluster` CTAs a unit.

@@ -40,6 +40,15 @@ EKV_DEV uint32_t split_pack(float f)
     return r;
 }
 
+// what hi + lo of split_pack leave of f, as bf16; f is the sum of the three to 2^-26
+EKV_DEV uint32_t split_rest(float f, uint32_t hilo)
+{
+    uint32_t r;
+    const float rest = f - bf16_bits_to_f32(hilo & 0xFFFFu) - __uint_as_float(hilo & 0xFFFF0000u);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(rest));
+    return r;
+}
+
 EKV_DEV void bar_consumers() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // Writes one row's joined result: a finished row, or a partial.
@@ -121,12 +130,17 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // Per CTA: a producer warp walks the share's pages and keeps a ring of
 // kRangeStages tiles (K and V, 64 tokens, 128-byte swizzle) full by TMA; four
 // consumer warps each own 16 tokens of every tile from scores to P.V, so no
-// block barrier stands between a tile's arrival and its release.  The query
-// (bf16 high + low part, columns 2h and 2h + 1) is the B operand of the score
-// product, its result's layout is turned in registers (movmatrix) into the B
-// operand of V^T P, and P again keeps a high and a low part: both splits leave
-// about 2^-17 of relative error where one bf16 would leave 2^-9.
-template <int D, int PS, int NT, bool CLUSTER>
+// block barrier stands between a tile's arrival and its release.  The query is
+// the B operand of the score product, its result's layout is turned in registers
+// (movmatrix) into the B operand of V^T P.  Both enter in bf16 parts: one would
+// leave 2^-9 of relative error, two 2^-18, three 2^-26.  The first two are columns
+// 2h and 2h + 1 of one product, the third is column 2h of a second into the same
+// accumulators.  A window takes three (REST): that doubles the products, which
+// the bytes hide but for 1.5% (64 sequences of 8192 + 64 tokens: 293.7 -> 298.1
+// us), and brings the error of 1028 tokens from 3.2e-6 to 3.2e-7 (2-norms; of 8192 from
+// 3.6e-6 to 2.7e-6, where the tensor cores' sums dominate).  The tokens behind a
+// shared prefix take two, as the prefix itself does.
+template <int D, int PS, int NT, bool CLUSTER, bool REST>
 __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                       const __grid_constant__ CUtensorMap vmap,
                                                                       const RangeArgs a, int cluster)
@@ -139,6 +153,9 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     float* red = reinterpret_cast<float*>(smem + 2 * kRangeStages * STAGE);   // [4 warps][4 heads][RED]
+    // the query's third parts, the same for all warps; red comes into use when they are done with
+    uint2* q_rest = reinterpret_cast<uint2*>(red);
+    static_assert(NT * KS * 32 * sizeof(uint2) <= 16 * RED * sizeof(float));
     __shared__ uint64_t full[kRangeStages], empty[kRangeStages];
     __shared__ int page_ok[kRangeStages];
     __shared__ float wm[2][4][4], wl[2][4][4];
@@ -261,12 +278,14 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
         if (!CLUSTER && tid == 0) range_note_span(a, w, u, nt, done, c_id);
 
         uint32_t bq[NT][KS][2];
+        if (REST) bar_consumers();                     // the last unit's reads of red are done
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             const int head = 4 * x + (gi >> 1);
             const float* qh = a.q + ((size_t)b * a.H_q + (size_t)w.g * a.G + head) * D;
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
+            for (int j = 0; j < KS; ++j) {
+                uint32_t third[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int k = 16 * j + 2 * c + 8 * e;
@@ -274,8 +293,12 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     const float v1 = head < a.G ? qh[k + 1] * a.xscale : 0.f;
                     const uint32_t p0 = split_pack(v0), p1 = split_pack(v1);
                     bq[x][j][e] = (gi & 1) ? __byte_perm(p0, p1, 0x7632) : __byte_perm(p0, p1, 0x5410);
+                    if (REST) third[e] = (gi & 1) ? 0u : __byte_perm(split_rest(v0, p0), split_rest(v1, p1), 0x5410);
                 }
+                if (REST && j % 4 == warp) q_rest[(x * KS + j) * 32 + lane] = make_uint2(third[0], third[1]);
+            }
         }
+        if (REST) bar_consumers();
         float acc[NT][MT][4], mrun[NT], lrun[NT];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -309,7 +332,13 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     uint32_t af[4];
                     ldsm_x4(swz_addr(kbase, row0 + (lane & 15), 2 * j + (lane >> 4)), af);
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) mma_bf16(sc[x], af, bq[x][j][0], bq[x][j][1]);
+                    for (int x = 0; x < NT; ++x) {
+                        mma_bf16(sc[x], af, bq[x][j][0], bq[x][j][1]);
+                        if (REST) {
+                            const uint2 t = q_rest[(x * KS + j) * 32 + lane];
+                            mma_bf16(sc[x], af, t.x, t.y);
+                        }
+                    }
                 }
                 if (masked) {
                     // a weight of zero must not meet a masked row's value: clear those rows of V
@@ -327,7 +356,7 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     fence_proxy_async();
                     __syncwarp();
                 }
-                uint32_t pb[NT][2];
+                uint32_t pb[NT][2], pr[NT][2];
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                     const float s0 = v_lo ? sc[x][0] + sc[x][1] : -INFINITY;
@@ -350,8 +379,13 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     }
                     const float p0 = exp2f(s0 - mu), p1 = exp2f(s1 - mu);
                     lrun[x] += p0 + p1;
-                    pb[x][0] = movmatrix_trans(split_pack(p0));
-                    pb[x][1] = movmatrix_trans(split_pack(p1));
+                    const uint32_t h0 = split_pack(p0), h1 = split_pack(p1);
+                    pb[x][0] = movmatrix_trans(h0);
+                    pb[x][1] = movmatrix_trans(h1);
+                    if (REST) {
+                        pr[x][0] = movmatrix_trans(split_rest(p0, h0));
+                        pr[x][1] = movmatrix_trans(split_rest(p1, h1));
+                    }
                 }
                 const int trow = row0 + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
@@ -359,7 +393,10 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                     uint32_t af[4];
                     ldsm_x4_t(swz_addr(vbase, trow, 2 * m + ((lane >> 3) & 1)), af);
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) mma_bf16(acc[x][m], af, pb[x][0], pb[x][1]);
+                    for (int x = 0; x < NT; ++x) {
+                        mma_bf16(acc[x][m], af, pb[x][0], pb[x][1]);
+                        if (REST) mma_bf16(acc[x][m], af, pr[x][0], pr[x][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -680,52 +717,49 @@ static int launch_range_kernel(void (*kern)(KArgs...), int C, int threads, int c
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 
-template <int D, int PS, bool CLUSTER>
+template <int D, int PS, bool CLUSTER, bool REST>
 static int launch_range_bf16(const RangeArgs& a, int C, int cluster, const CUtensorMap* kmap, const CUtensorMap* vmap,
                              cudaStream_t stream)
 {
     const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024;
-    return a.G == 8 ? launch_range_kernel(range_bf16_kernel<D, PS, 2, CLUSTER>, C, kRangeThreads, cluster, smem, stream,
-                                          *kmap, *vmap, a)
-                    : launch_range_kernel(range_bf16_kernel<D, PS, 1, CLUSTER>, C, kRangeThreads, cluster, smem, stream,
-                                          *kmap, *vmap, a);
+    const auto kern = a.G == 8 ? range_bf16_kernel<D, PS, 2, CLUSTER, REST> : range_bf16_kernel<D, PS, 1, CLUSTER, REST>;
+    return launch_range_kernel(kern, C, kRangeThreads, cluster, smem, stream, *kmap, *vmap, a);
 }
 
-template <int D, bool CLUSTER>
+template <int D, bool CLUSTER, bool REST>
 static int launch_range_d(const entmaxkv_pool& pool, const RangeArgs& a, int C, int cluster, const CUtensorMap* kmap,
                           const CUtensorMap* vmap, cudaStream_t stream)
 {
     if (pool.dtype == ENTMAXKV_F32) {
-        const float* k = (const float*)pool.k_pool;
-        const float* v = (const float*)pool.v_pool;
-        return a.G == 8 ? launch_range_kernel(range_f32_kernel<D, 8, CLUSTER>, C, 128, cluster, RangeF32<D, 8>::SMEM, stream,
-                                              k, v, pool.ps, a)
-                        : launch_range_kernel(range_f32_kernel<D, 4, CLUSTER>, C, 128, cluster, RangeF32<D, 4>::SMEM, stream,
-                                              k, v, pool.ps, a);
+        const auto kern = a.G == 8 ? range_f32_kernel<D, 8, CLUSTER> : range_f32_kernel<D, 4, CLUSTER>;
+        const int smem = a.G == 8 ? RangeF32<D, 8>::SMEM : RangeF32<D, 4>::SMEM;
+        return launch_range_kernel(kern, C, 128, cluster, smem, stream, (const float*)pool.k_pool,
+                                   (const float*)pool.v_pool, pool.ps, a);
     }
-    return pool.ps == 64 ? launch_range_bf16<D, 64, CLUSTER>(a, C, cluster, kmap, vmap, stream)
-                         : launch_range_bf16<D, 16, CLUSTER>(a, C, cluster, kmap, vmap, stream);
+    return pool.ps == 64 ? launch_range_bf16<D, 64, CLUSTER, REST>(a, C, cluster, kmap, vmap, stream)
+                         : launch_range_bf16<D, 16, CLUSTER, REST>(a, C, cluster, kmap, vmap, stream);
 }
 
 int launch_range(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                  const CUtensorMap* vmap, cudaStream_t stream)
 {
-    return pool.d == 128 ? launch_range_d<128, false>(pool, a, C, 0, kmap, vmap, stream)
-                         : launch_range_d<64, false>(pool, a, C, 0, kmap, vmap, stream);
+    return pool.d == 128 ? launch_range_d<128, false, false>(pool, a, C, 0, kmap, vmap, stream)
+                         : launch_range_d<64, false, false>(pool, a, C, 0, kmap, vmap, stream);
 }
 
 int launch_window_cluster(const entmaxkv_pool& pool, const RangeArgs& a, int cluster, const CUtensorMap* kmap,
                           const CUtensorMap* vmap, cudaStream_t stream)
 {
     const int C = a.B * a.H_kv * cluster;
-    return pool.d == 128 ? launch_range_d<128, true>(pool, a, C, cluster, kmap, vmap, stream)
-                         : launch_range_d<64, true>(pool, a, C, cluster, kmap, vmap, stream);
+    return pool.d == 128 ? launch_range_d<128, true, true>(pool, a, C, cluster, kmap, vmap, stream)
+                         : launch_range_d<64, true, true>(pool, a, C, cluster, kmap, vmap, stream);
 }
 
 int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CUtensorMap* kmap,
                   const CUtensorMap* vmap, cudaStream_t stream)
 {
-    const int rc = launch_range(pool, a, C, kmap, vmap, stream);
+    const int rc = pool.d == 128 ? launch_range_d<128, false, true>(pool, a, C, 0, kmap, vmap, stream)
+                                 : launch_range_d<64, false, true>(pool, a, C, 0, kmap, vmap, stream);
     if (rc) return rc;
     const int n = a.B * a.H_kv;
     const auto merge = merge_threads(n) == 1024
