@@ -611,7 +611,8 @@ int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, in
     }
     PrefixArgs a{};
     a.r = range_args(*pool, q, H_q, page_table, max_pages, seq_lens, B, scale, out, lse_out, ws, lay.range, status);
-    const double most = (double)B * max_pages * pool->ps * pool->H_kv * pool->d * (pool->dtype == ENTMAXKV_BF16 ? 4 : 8);
+    const double most =
+        (double)B * max_pages * pool->ps * pool->H_kv * pool->d * (pool->dtype == ENTMAXKV_BF16 ? 4 : 8);
     // (a query off 16 bytes goes there too: those kernels read it word by word)
     if (n_groups == 0 || most < kPrefixLeastBytes || !aligned16(q)) {
         a.r.window = INT32_MAX;

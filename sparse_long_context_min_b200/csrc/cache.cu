@@ -117,16 +117,16 @@ EKV_DEV void copy_chunk(const PageBytes& pb, int src, int dst, int chunk)
 
 // Many pages: one warp a CTA moves chunks through a ring in shared memory with
 // bulk copies in both directions, so that what is in flight does not go by
-// threads and registers (the copies through registers above ran at 58% of a plain
-// copy's rate: profiled at 251 pages of 268 KB, 35 us).  `pick` gives the pages of copy i, or
-// false to skip it.
+// threads and registers.  Measured (the kernel alone, profiled) at 251 pages of
+// 268 KB: 21.7 us, 6.2 TB/s read and written, against 34.7 us by way of
+// registers as above.  `pick` gives the pages of copy i, or false to skip it.
 constexpr int kRingSlots = 3, kRingCtas = 4;           // 48 KB a CTA, four CTAs an SM
 constexpr int kRingBytes = kRingSlots * kCopyChunk;
 
 EKV_DEV void bulk_store(void* dst, const void* src, uint32_t bytes)
 {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
-                 : "memory");
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                 ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 

@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
         auto load_q = [&] {
             const PrefixGroup& G = a.groups[w.j];
             const int r = w.t * kPfxRows + row;
-            const float* q = a.r.q + ((size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1))) * D +
-                             quarter * QD;
+            const size_t at_q = (size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1));
+            const float* q = a.r.q + at_q * D + quarter * QD;
 #pragma unroll
             for (int e = 0; e < QD / 4; ++e)
                 qv[e] = r < G.rows ? reinterpret_cast<const float4*>(q)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             for (int e = 0; e < QD / 2; ++e) {
                 const float2 x = make_float2(v[2 * e] * a.r.xscale, v[2 * e + 1] * a.r.xscale);
                 hi[e] = bf16x2(x);
-                lo[e] = bf16x2(make_float2(x.x - __uint_as_float(hi[e] << 16), x.y - __uint_as_float(hi[e] & 0xffff0000u)));
+                lo[e] = bf16x2(make_float2(x.x - __uint_as_float(hi[e] << 16),
+                                           x.y - __uint_as_float(hi[e] & 0xffff0000u)));
             }
             const uint32_t dst = Q + lanes + quarter * (QD / 2);
 #pragma unroll
@@ -841,7 +842,8 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int e = 0; e < W; e += 2) {
-                        const float2 o = unpair(fma2(pair(pt[j], pt[j]), pair(v[e], v[e + 1]), pair(acc[j][e], acc[j][e + 1])));
+                        const float2 o = unpair(
+                            fma2(pair(pt[j], pt[j]), pair(v[e], v[e + 1]), pair(acc[j][e], acc[j][e + 1])));
                         acc[j][e] = o.x;
                         acc[j][e + 1] = o.y;
                     }
@@ -868,7 +870,8 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
                 if (r8 + j < rows) {
                     const float2 x = ml[r8 + j];
                     const float M = fmaxf(m[j], x.x);
-                    const float f0 = m[j] == -INFINITY ? 0.f : exp2f(m[j] - M), f1 = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
+                    const float f0 = m[j] == -INFINITY ? 0.f : exp2f(m[j] - M);
+                    const float f1 = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
                         const int d = lane * W + e;
@@ -941,8 +944,8 @@ static int launch_prefix_f32(const entmaxkv_pool& pool, const PrefixArgs& a, cud
 {
     const int smem = PfxF32<D>::FLOATS * 4;
     if (ensure_smem((const void*)prefix_f32_kernel<D, PS>, smem)) return ENTMAXKV_CUDA_ERROR;
-    return launch_pdl(prefix_f32_kernel<D, PS>, dim3(a.C), dim3(kPfxThreadsF32), smem, stream, (const float*)pool.k_pool,
-                      (const float*)pool.v_pool, a) == cudaSuccess
+    return launch_pdl(prefix_f32_kernel<D, PS>, dim3(a.C), dim3(kPfxThreadsF32), smem, stream,
+                      (const float*)pool.k_pool, (const float*)pool.v_pool, a) == cudaSuccess
                ? ENTMAXKV_OK
                : ENTMAXKV_CUDA_ERROR;
 }
@@ -971,8 +974,8 @@ int launch_prefix(const entmaxkv_pool& pool, const PrefixArgs& a, int range_C, c
     const auto merge = merge_threads(n) == 1024
                            ? (pool.d == 128 ? prefix_merge_kernel<128, 1024> : prefix_merge_kernel<64, 1024>)
                            : (pool.d == 128 ? prefix_merge_kernel<128, 256> : prefix_merge_kernel<64, 256>);
-    return launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, a) == cudaSuccess ? ENTMAXKV_OK
-                                                                                          : ENTMAXKV_CUDA_ERROR;
+    const cudaError_t e = launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, a);
+    return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 
 }  // namespace ekv

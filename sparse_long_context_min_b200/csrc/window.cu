@@ -540,8 +540,9 @@ __global__ void __launch_bounds__(128, 2) range_f32_kernel(const float* __restri
                 phys = phys_next;
                 pos = pos_next;
                 phys_next = lookup(it / STEPS + 1, pos_next);
-                if (phys >= a.num_phys || (phys < 0 && it < last &&
-                                           div_ps((long long)(w.t + it / STEPS) * kRangeTile + warp * 16, ps) < sp.pages())) {
+                const bool walked =
+                    it < last && div_ps((long long)(w.t + it / STEPS) * kRangeTile + warp * 16, ps) < sp.pages();
+                if (walked && (phys < 0 || phys >= a.num_phys)) {
                     report(a.status, ENTMAXKV_DEVICE_BOUNDS);
                     phys = -1;
                 }
@@ -712,8 +713,9 @@ static int launch_range_kernel(void (*kern)(KArgs...), int C, int threads, int c
 {
     if (smem && ensure_smem((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
     if (cluster > 8 && ensure_cluster_kernel((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
-    const cudaError_t e = cluster ? launch_pdl_cluster(kern, dim3(C), dim3(threads), cluster, smem, stream, args..., cluster)
-                                  : launch_pdl(kern, dim3(C), dim3(threads), smem, stream, args..., cluster);
+    const dim3 grid(C), block(threads);
+    const cudaError_t e = cluster ? launch_pdl_cluster(kern, grid, block, cluster, smem, stream, args..., cluster)
+                                  : launch_pdl(kern, grid, block, smem, stream, args..., cluster);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 
@@ -722,7 +724,8 @@ static int launch_range_bf16(const RangeArgs& a, int C, int cluster, const CUten
                              cudaStream_t stream)
 {
     const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024;
-    const auto kern = a.G == 8 ? range_bf16_kernel<D, PS, 2, CLUSTER, REST> : range_bf16_kernel<D, PS, 1, CLUSTER, REST>;
+    const auto kern =
+        a.G == 8 ? range_bf16_kernel<D, PS, 2, CLUSTER, REST> : range_bf16_kernel<D, PS, 1, CLUSTER, REST>;
     return launch_range_kernel(kern, C, kRangeThreads, cluster, smem, stream, *kmap, *vmap, a);
 }
 
@@ -765,8 +768,8 @@ int launch_window(const entmaxkv_pool& pool, const RangeArgs& a, int C, const CU
     const auto merge = merge_threads(n) == 1024
                            ? (pool.d == 128 ? range_merge_kernel<128, 1024> : range_merge_kernel<64, 1024>)
                            : (pool.d == 128 ? range_merge_kernel<128, 256> : range_merge_kernel<64, 256>);
-    return launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, pool.ps, a) == cudaSuccess ? ENTMAXKV_OK
-                                                                                                   : ENTMAXKV_CUDA_ERROR;
+    const cudaError_t e = launch_pdl(merge, dim3(n), dim3(merge_threads(n)), 0, stream, pool.ps, a);
+    return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_CUDA_ERROR;
 }
 
 }  // namespace ekv

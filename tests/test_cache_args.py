@@ -116,13 +116,13 @@ def _cpool(num=20, H_kv=8, ps=64, d=128, dtype=B.BF16, base=256):
 
 def _window(pool=None, q=P, H_q=32, table=P, max_pages=10, lens=P, n=3, window=5, sinks=0, scale=0.1, out=P, ws=P,
             size=BIG, status=P):
-    return B.lib().entmaxkv_window_softmax_decode(pool or _cpool(), q, H_q, table, max_pages, lens, n, window, sinks, scale,
-                                                  out, None, ws, size, status, None)
+    return B.lib().entmaxkv_window_softmax_decode(pool or _cpool(), q, H_q, table, max_pages, lens, n, window, sinks,
+                                                  scale, out, None, ws, size, status, None)
 
 
 def _prefix(pool=None, H_q=32, max_pages=10, n=3, starts=P, prefixes=P, groups=2, scale=0.1, ws=P, size=BIG, status=P):
-    return B.lib().entmaxkv_prefix_softmax_decode(pool or _cpool(), P, H_q, P, max_pages, P, n, starts, prefixes, groups,
-                                                  scale, P, None, ws, size, status, None)
+    return B.lib().entmaxkv_prefix_softmax_decode(pool or _cpool(), P, H_q, P, max_pages, P, n, starts, prefixes,
+                                                  groups, scale, P, None, ws, size, status, None)
 
 
 def test_window_and_prefix_validate_on_the_host():

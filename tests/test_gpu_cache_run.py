@@ -54,8 +54,8 @@ class Server:
         kv = torch.randn(2, 1, H_KV, n, D, generator=g).to(self.dtype)
         B.append_metadata(self.pool, kv[0].cuda(), kv[1].cuda(), self.table[:1], self.lens[:1], self.status)
         i32 = dict(dtype=torch.int32, device="cuda")
-        B.fork_sequences(self.pool, self.ref, self.table, self.lens, torch.zeros(3, **i32), torch.tensor([1, 2, 3], **i32),
-                         self.ws, self.status)
+        B.fork_sequences(self.pool, self.ref, self.table, self.lens, torch.zeros(3, **i32),
+                         torch.tensor([1, 2, 3], **i32), self.ws, self.status)
         self.prefixes.fill_(n)
         for b in range(4):
             self.keys[b], self.vals[b] = (x[0].transpose(0, 1).double().numpy() for x in kv)
@@ -177,7 +177,8 @@ def test_a_pool_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     for call in (lambda: B.copy_pages(s.pool, s.lens[:1], s.lens[:1], s.ws, s.status),
                  lambda: B.free_pages(s.pool, s.ref, s.table, s.lens, None, s.status),
-                 lambda: B.window_softmax_decode(s.pool, s.q, s.table, s.lens, 5, 0, 0.1, s.out["window"], s.ws, s.status)):
+                 lambda: B.window_softmax_decode(s.pool, s.q, s.table, s.lens, 5, 0, 0.1, s.out["window"], s.ws,
+                                                 s.status)):
         with pytest.raises(B.EntmaxKVError, match="the pool is on cuda:0, the current device is cuda:1"):
             call()
 
