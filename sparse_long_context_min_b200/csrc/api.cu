@@ -420,9 +420,9 @@ static int pages_check(const entmaxkv_pool* pool, int max_pages, int B)
     int rc = check_pool(pool, true, true);
     if (rc) return rc;
     if (B < 0 || max_pages <= 0) return ENTMAXKV_INVALID_ARG;
-    // 32-bit counts of table entries and of a page's bytes, and the bitmap of
-    // the counting cluster (200 KB in each of its 8 CTAs)
-    if ((long long)B * max_pages > INT32_MAX || pool->H_kv > 65535 || pool->num_phys_pages > 13000000)
+    // 32-bit counts of table entries and of a page's bytes, rows of 65535 chunks,
+    // and the bitmap of the counting cluster (200 KB in each of its 8 CTAs)
+    if ((long long)B * max_pages > INT32_MAX || max_pages > 65535 * 1024 || pool->H_kv > 65535 || pool->num_phys_pages > 13000000)
         return ENTMAXKV_UNSUPPORTED;
     return ENTMAXKV_OK;
 }

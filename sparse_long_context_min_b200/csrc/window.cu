@@ -712,7 +712,13 @@ static int launch_range_kernel(void (*kern)(KArgs...), int C, int threads, int c
                                Args&&... args)
 {
     if (smem && ensure_smem((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
-    if (cluster > 8 && ensure_cluster_kernel((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
+    if (cluster > 8) {
+        if (ensure_cluster_kernel((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
+        if (max_active_clusters((const void*)kern, cluster, threads, smem) == 0) {   // no GPC holds so many
+            C = C / cluster * 8;
+            cluster = 8;
+        }
+    }
     const dim3 grid(C), block(threads);
     const cudaError_t e = cluster ? launch_pdl_cluster(kern, grid, block, cluster, smem, stream, args..., cluster)
                                   : launch_pdl(kern, grid, block, smem, stream, args..., cluster);

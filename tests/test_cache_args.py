@@ -180,6 +180,7 @@ def test_page_calls_validate_on_the_host():
         if call is not free:
             assert call(ws=None) == B.WORKSPACE
             assert call(size=100) == B.WORKSPACE
+    assert free(rows=1, max_pages=65535 * 1024 + 1, n=1) == B.UNSUPPORTED   # a row of more chunks than a grid has
     assert copy(n=-1) == B.INVALID_ARG and copy(src=None) == B.INVALID_ARG and copy(n=0) == B.OK
     assert fork(n=5) == B.INVALID_ARG and fork(n=-1) == B.INVALID_ARG and fork(n=0) == B.OK
     assert free(n=-1) == B.INVALID_ARG and free(sinks=-1) == B.INVALID_ARG and free(n=0) == B.OK
