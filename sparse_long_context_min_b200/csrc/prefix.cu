@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
         // ---------------------------------------------------- producer
         int it = 0;                                    // ring slots filled so far
         auto load = [&](const CUtensorMap* map, int g, int ph) {
-            // lanes < PPB hold the block's physical pages (-1: none)
+            // lanes < PPB hold the block's physical pages (negative: none)
             const int slot = it % SLOTS;
             const bool go = it < SLOTS || pfx_wait(&empty[slot], (uint32_t)((it / SLOTS - 1) & 1), &dead, status);
             const uint32_t good = __ballot_sync(0xffffffffu, lane < PPB && ph >= 0);
@@ -548,13 +548,13 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             const PrefixGroup& G = a.groups[w.j];
             const int g = w.g;
             const int32_t* pages = a.r.page_table + (size_t)G.first * a.r.max_pages;
-            // 32 blocks' pages at a time would hide their loads; one block ahead does, behind the ring
-            auto page = [&](int blk) {
-                if (lane >= PPB) return -1;
+            // 32 pages at a time, one a lane, so that their loads are waited for once
+            const int end = (k + n) * PPB;
+            auto page = [&](int p) {
+                if (p >= end) return -1;
                 // pages past the shared ones repeat the block's first page: their scores are masked, and
                 // the weight of zero they get must meet a value that some row uses anyway
-                int p = blk * PPB + lane;
-                if (p >= G.pages) p = blk * PPB;
+                if (p >= G.pages) p &= ~(PPB - 1);
                 const int ph = pages[p];
                 if (ph < 0 || ph >= a.r.num_phys) {
                     report(status, ENTMAXKV_DEVICE_BOUNDS);
@@ -562,13 +562,14 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                 }
                 return ph;
             };
-            int ph = page(k), prev = -1;
+            int batch = -1, prev = -1;
             for (int i = 0; i <= n && go; ++i) {
-                const int next = i + 1 < n ? page(k + i + 1) : -1;
+                const int at = i * PPB & 31;
+                if (at == 0) batch = page((k + i) * PPB + lane);
+                const int ph = __shfl_sync(0xffffffffu, batch, (at + lane) & 31);
                 if (i < n) go = load(&kmap, g, ph);
                 if (i > 0 && go) go = load(&vmap, g, prev);
                 prev = ph;
-                ph = next;
             }
         }
         if (!go && lane == 0)
