@@ -199,6 +199,12 @@ EKV_DEV void tc_st16(uint32_t addr, const uint32_t* r)
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
                  ::EKV_W8(r, 0), EKV_W8(r, 8), "r"(addr) : "memory");
 }
+// 16 lanes x 8 columns: a thread's words are columns 2 (lane % 4) and the next, of rows lane / 4 and lane / 4 + 8
+EKV_DEV void tc_st_16x256(uint32_t addr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%4], {%0, %1, %2, %3};"
+                 ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(addr) : "memory");
+}
 EKV_DEV void tc_st8(uint32_t addr, const uint32_t* r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
@@ -368,32 +374,43 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t at = S[set] + lanes + half * 32, acc = O[set] + lanes + half * (D / 2);
         const int lg = __ffs(a.r.G) - 1;
-        float4 qv[QD / 4];                             // this thread's part of its row's query
+        // Q goes to tensor memory in blocks of 16 rows x 16 dims: a lane holds four dims of rows lane / 4 and
+        // lane / 4 + 8 of each, so that four lanes read 64 consecutive bytes (a row a lane took 3 us longer to
+        // fetch 128 rows)
+        constexpr int QB = QD / 16;                    // such blocks along this warp's dims
+        float4 qv[2][QB][2];
         auto load_q = [&] {
             const PrefixGroup& G = a.groups[w.j];
-            const int r = w.t * kPfxRows + row;
-            const size_t at_q = (size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1));
-            const float* q = a.r.q + at_q * D + quarter * QD;
 #pragma unroll
-            for (int e = 0; e < QD / 4; ++e)
-                qv[e] = r < G.rows ? reinterpret_cast<const float4*>(q)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 4; ++i) {
+                const int r = w.t * kPfxRows + quad * 32 + i * 8 + (lane >> 2);
+                const size_t at_q = (size_t)(G.lo + (r >> lg)) * a.r.H_q + ((size_t)w.g << lg) + (r & (a.r.G - 1));
+                const float* q = a.r.q + at_q * D + quarter * QD + (lane & 3) * 4;
+#pragma unroll
+                for (int e = 0; e < QB; ++e)
+                    qv[i / 2][e][i % 2] = r < G.rows ? *reinterpret_cast<const float4*>(q + e * 16)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         };
         auto stage_q = [&] {
-            uint32_t hi[QD / 2], lo[QD / 2];
-            const float* v = reinterpret_cast<const float*>(qv);
 #pragma unroll
-            for (int e = 0; e < QD / 2; ++e) {
-                const float2 x = make_float2(v[2 * e] * a.r.xscale, v[2 * e + 1] * a.r.xscale);
-                hi[e] = bf16x2(x);
-                lo[e] = bf16x2(make_float2(x.x - __uint_as_float(hi[e] << 16),
-                                           x.y - __uint_as_float(hi[e] & 0xffff0000u)));
-            }
-            const uint32_t dst = Q + lanes + quarter * (QD / 2);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < QD / 2; e += 8) {
-                tc_st8(dst + e, hi + e);
-                tc_st8(dst + D / 2 + e, lo + e);
-            }
+                for (int e = 0; e < QB; ++e) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 v = qv[i][e][k / 2];
+                        const float2 x = k % 2 ? make_float2(v.z * a.r.xscale, v.w * a.r.xscale)
+                                               : make_float2(v.x * a.r.xscale, v.y * a.r.xscale);
+                        hi[k] = bf16x2(x);
+                        lo[k] = bf16x2(make_float2(x.x - __uint_as_float(hi[k] << 16),
+                                                   x.y - __uint_as_float(hi[k] & 0xffff0000u)));
+                    }
+                    const uint32_t dst = Q + lanes + (i << 20) + quarter * (QD / 2) + e * 8;
+                    tc_st_16x256(dst, hi);
+                    tc_st_16x256(dst + D / 2, lo);
+                }
             if (half == 0) top_of[set][row] = ordered_int(-INFINITY);
             tc_wait_st();
             tc_fence_before();
