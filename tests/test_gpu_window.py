@@ -126,6 +126,15 @@ def test_window_large_scores(dtype):
     check_window(c, 1500, 3)
 
 
+@pytest.mark.parametrize("d,ps,spread", [(64, 64, 1.0), (64, 64, 20.0), (128, 16, 3.0)])
+def test_window_long_shares(d, ps, spread):
+    """Enough tiles that a CTA has more than 32 of one unit: its accumulators are emptied on the way."""
+    rng = np.random.default_rng(2)
+    lens = [int(x) for x in rng.integers(4200, 4600, size=24)]
+    c = Cache(lens, 32, 8, d, ps, BF16, visible=lambda L: ranges.window_tokens(L, 4190, 5), seed=11, spread=spread)
+    check_window(c, 4190, 5)
+
+
 def test_window_many_sequences():
     """More sequences than a block has threads, half of them empty, and units cut anywhere."""
     rng = np.random.default_rng(5)
