@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kRowThreads) fork_apply_kernel(const ForkArgs 
     const int i = unit / per, part = unit % per;
     const int need = a.want[i];
     if (!row && need == 0) return;                     // also: refused forks need none
-    if (!fork_fine(a, i)) return;
+    if (row && !fork_fine(a, i)) return;
     const int s = a.src[i], d = a.dst[i];
     const int L = a.seq_lens[s];
     const int at = a.at[i];
