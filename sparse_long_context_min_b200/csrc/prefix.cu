@@ -276,6 +276,11 @@ EKV_DEV uint32_t bf16x2(float2 v)
 // bound the time; more rows than a tile's 128 make the products bound it.  O is
 // rescaled only when the maximum grew by more than 2^8, which keeps every
 // weight in range and rescaling rare.
+//
+// Measured (the kernel alone, profiled; 8 kv heads of 128 dims): 128 rows behind
+// 131072 tokens 107 us, 5.0 TB/s; 384 rows behind 32809 84 us, the tensor pipe busy
+// 64% of the time (1275 cycles a block, of which the product warp waits a fifth).
+// With blocks of 128 tokens and Q in shared memory the latter took 118 us.
 constexpr int kPfxRows = 128, kPfxTok = 64;
 constexpr int kPfxSoft = 16;             // softmax warps
 constexpr int kPfxThreads = (kPfxSoft + 2) * 32;

