@@ -350,7 +350,8 @@ ENTMAXKV_API int entmaxkv_window_softmax_decode(const entmaxkv_pool* pool, const
  *   prefix_lens [n_groups] int32: the first prefix_lens[j] tokens are the same
  *     for the whole group, and the page-table rows of its sequences name the same
  *     physical pages for the whole pages among them (as entmaxkv_fork_sequences
- *     leaves them): the library reads these pages through the group's first row.
+ *     leaves them): the library reads these pages through the group's first row
+ *     that is not empty (or, in small calls, through each row).
  *     Tokens behind the last whole page, and those behind the group's shortest
  *     non-empty sequence, are read through each sequence's own row.
  *   0 <= n_groups <= B (0: group_start and prefix_lens may be NULL).
