@@ -27,21 +27,25 @@ int num_sms()
 
 int ensure_smem(const void* func, int bytes)
 {
-    // one flag per (kernel, device); a small table of seen pairs
+    // the largest limit set so far per (kernel, device), in a small table: some
+    // kernels' shared memory grows with the problem
+    struct Entry {
+        const void* f;
+        int dev, bytes;
+    };
     static std::mutex mu;
-    static const void* seen_f[1024];
-    static int seen_d[1024];
+    static Entry seen[1024];
     static int nseen = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < nseen; ++i)
-        if (seen_f[i] == func && seen_d[i] == dev) return 0;
+    int i = 0;
+    while (i < nseen && (seen[i].f != func || seen[i].dev != dev)) ++i;
+    if (i < nseen && seen[i].bytes >= bytes) return 0;
     if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return 1;
-    if (nseen < 1024) {
-        seen_f[nseen] = func;
-        seen_d[nseen] = dev;
-        ++nseen;
+    if (i < 1024) {
+        seen[i] = Entry{func, dev, bytes};
+        if (i == nseen) ++nseen;
     }
     return 0;
 }

@@ -725,8 +725,8 @@ static int done(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXK
 template <typename... KArgs, typename... Args>
 static int launch_cluster(void (*kern)(KArgs...), const PlanArgs& a, cudaStream_t stream, const Args&... args)
 {
-    const int smem = a.slice / 8;
-    if (smem > 48 * 1024 && ensure_smem((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
+    const int smem = a.slice / 8;                      // a bit a page: grows with the pool
+    if (ensure_smem((const void*)kern, smem)) return ENTMAXKV_CUDA_ERROR;
     return done(launch_pdl_cluster(kern, dim3(kPlanCluster), dim3(kPlanThreads), kPlanCluster, smem, stream, args...));
 }
 

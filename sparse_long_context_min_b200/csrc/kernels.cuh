@@ -97,14 +97,14 @@ int launch_compact(const entmaxkv_pool& pool, int32_t* ref, int32_t* page_table,
 
 int launch_selftest_timeout(int64_t limit_ns, int32_t* status, cudaStream_t stream);
 
-// set the dynamic shared memory limit of a kernel once per device
+// raise the dynamic shared memory limit of a kernel on the current device to at least `bytes`
 int ensure_smem(const void* func, int bytes);
 
 // SM count of the current device
 int num_sms();
 
 // Dynamic shared memory limit and permission for clusters above 8 CTAs of a
-// cluster kernel, once per device.
+// cluster kernel on the current device.
 int ensure_cluster_kernel(const void* func, int smem);
 
 // Clusters of `cluster` CTAs (threads, smem each) the current device can run
