@@ -438,9 +438,11 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
 
             float m = -INFINITY, l = 0.f;
             for (int i = set; i < n; i += 2, ++s_n) {
-                const bool ok = pfx_wait(&s_full[set], s_n & 1, &dead, status);
+                // whatever comes of the wait: the other half's warp counts on this one at the barrier below,
+                // and scores that never came do no harm (the status says so)
+                pfx_wait(&s_full[set], s_n & 1, &dead, status);
                 tc_fence_after();
-                if (ok && quad * 32 < rows) {
+                if (quad * 32 < rows) {
                     uint32_t s[32];
                     tc_ld32(at, s);
                     tc_wait_ld<32>(s);
