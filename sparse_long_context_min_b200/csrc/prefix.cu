@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
     constexpr int QD = D / 4;                          // dims of a row that one thread stages
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align<1024>(smem_raw);
-    __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], q_full, o_full;
+    __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], q_full, o_full, drained;
     __shared__ uint32_t tmem_slot;
     __shared__ PrefixWalk start;
     __shared__ int top_of[2][kPfxRows];                // [set][row] largest score so far, as an ordered integer
@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
         }
         mbar_init(&q_full, kPfxSoft);
         mbar_init(&o_full, 1);
+        mbar_init(&drained, 1);
         fence_mbar_init();
         dead = 0;
         prefetch_tmap(&kmap);
@@ -596,7 +597,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                 prev = ph;
             }
         }
-        if (!go && lane == 0)
+        // nothing may be on its way when the CTA ends (roles that gave up do not wait for it)
+        if (lane == 0)
             for (int i = max(0, it - SLOTS); i < it; ++i)
                 mbar_wait(&full[i % SLOTS], (uint32_t)((i / SLOTS) & 1), kWaitLimitNs);
     } else {
@@ -671,6 +673,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             __syncwarp();
             ++seg;
         }
+        // nor may products (where the softmax warps gave up, nobody has waited for them)
+        if (elect_one()) tc_commit(&drained);
+        __syncwarp();
+        if (!mbar_wait(&drained, 0, kWaitLimitNs)) report(status, ENTMAXKV_TIMEOUT);
     }
     tc_fence_before();
     __syncthreads();
@@ -776,7 +782,7 @@ __global__ void __launch_bounds__(kPfxThreadsF32, 1) prefix_f32_kernel(const flo
                               PS * D * 4, &v_full[slot]);
             }
         }
-        if (!go && lane == 0)                          // and so must the blocks before
+        if (lane == 0)                                 // and so must the blocks before, whoever gave up
             for (int i = max(0, it - 2); i < it; ++i) {
                 mbar_wait(&k_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
                 mbar_wait(&v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);

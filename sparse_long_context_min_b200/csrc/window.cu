@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
             }
             advance(n);
         }
-        // nothing of this CTA's is in flight once the last tiles have landed
-        if (stop && lane == 0)
+        // nothing of this CTA's is in flight once the last tiles have landed (consumers that gave up do not
+        // wait for them)
+        if (lane == 0)
             for (long long i = max(0ll, issued - kRangeStages); i < issued; ++i)
                 mbar_wait(&full[i % kRangeStages], (uint32_t)((i / kRangeStages) & 1), kWaitLimitNs);
         w.left = 0;
