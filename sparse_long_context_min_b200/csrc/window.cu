@@ -20,7 +20,6 @@ namespace ekv {
 
 constexpr int kRangeStages = 3;
 constexpr int kRangeThreads = 160;       // four consumer warps and a producer warp
-constexpr int kFlushTiles = 32;
 constexpr int kRedPad = 8;               // padding (floats) of a row of the joining buffer
 
 // D = A.trans on 8x8 16-bit matrices held one row per four lanes
@@ -138,12 +137,15 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // 2h and 2h + 1 of one product, the third is column 2h of a second into the same
 // accumulators.  A window takes three (REST): that doubles the products, which
 // the bytes hide but for 1.5% (64 sequences of 8192 + 64 tokens: 293.7 -> 298.1
-// us), and brings the error of 1028 tokens from 3.2e-6 to 3.3e-7 (2-norms).  Over
-// long shares the tensor cores' sums, which are cut off and not rounded, took over
-// (2.7e-6 at 8256 tokens): every kFlushTiles tiles the accumulators are emptied
-// into shared memory by rounded adds (1.1e-6, 300.7 us; every 16 tiles 7.5e-7,
-// 303.8 us).  Groups of 8 heads leave no room for that.  The tokens behind a
-// shared prefix take two parts, as the prefix itself does.
+// us), and brings the error of 1028 tokens from 3.2e-6 to 3.6e-7 (2-norms).  The
+// tokens behind a shared prefix take two parts, as the prefix itself does (3.5e-6).
+// The tensor cores cut their sums off and do not round them, always to the same
+// side: left in their accumulators, a sum loses 8e-8 of itself a tile (8e-5 at
+// 65536 tokens of values around 1).  So the products of a warp's 16 tokens start
+// from zero and are added to the output by rounded adds (2.5e-7 there, as plain
+// fp32 sums have).  Two slices of 16 dims at a time, so that no product waits for
+// the one before: 64 windows of 8256 tokens 302 us at 4 heads a group, 331 at 8
+// (one slice at a time 367).
 template <int D, int PS, int NT, bool CLUSTER, bool REST>
 __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                       const __grid_constant__ CUtensorMap vmap,
@@ -154,12 +156,11 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
     constexpr int PPS = kRangeTile / PS;
     constexpr int KS = D / 16, MT = D / 16;
     constexpr int RED = D + kRedPad;
-    constexpr bool FLUSH = REST && NT == 1;            // (with NT 2 there is no room, and q_rest lies in red)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     float* red = reinterpret_cast<float*>(smem + 2 * kRangeStages * STAGE);   // [4 warps][4 heads][RED]
-    // the query's third parts, the same for all warps
-    uint2* q_rest = reinterpret_cast<uint2*>(FLUSH ? red + 16 * RED : red);
+    // the query's third parts, the same for all warps, until the unit's results take their place
+    uint2* q_rest = reinterpret_cast<uint2*>(red);
     static_assert(NT * KS * 32 * sizeof(uint2) <= 16 * RED * sizeof(float));
     __shared__ uint64_t full[kRangeStages], empty[kRangeStages];
     __shared__ int page_ok[kRangeStages];
@@ -305,16 +306,14 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
             }
         }
         if (REST) bar_consumers();
-        float acc[NT][MT][4], mrun[NT], lrun[NT];
+        float acc[NT][MT][2], mrun[NT], lrun[NT];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             mrun[x] = -INFINITY;
             lrun[x] = 0.f;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[x][m][0] = acc[x][m][1] = acc[x][m][2] = acc[x][m][3] = 0.f;
+            for (int m = 0; m < MT; ++m) acc[x][m][0] = acc[x][m][1] = 0.f;
         }
-        bool kept = false;                             // outputs of earlier tiles lie in red, at the maximum mkept
-        float mkept = -INFINITY;
         for (int k = 0; k < n; ++k, ++tile) {
             const int slot = (int)(tile % kRangeStages);
             const bool ok = !dead && mbar_wait(&full[slot], (uint32_t)((tile / kRangeStages) & 1), kWaitLimitNs);
@@ -380,8 +379,8 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                         lrun[x] *= corr;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            acc[x][m][0] *= corr; acc[x][m][1] *= corr;
-                            acc[x][m][2] *= corr; acc[x][m][3] *= corr;
+                            acc[x][m][0] *= corr;
+                            acc[x][m][1] *= corr;
                         }
                         mrun[x] = mnew;
                     }
@@ -397,33 +396,32 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
                 }
                 const int trow = row0 + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t af[4];
-                    ldsm_x4_t(swz_addr(vbase, trow, 2 * m + ((lane >> 3) & 1)), af);
+                for (int m0 = 0; m0 < MT; m0 += 2) {
+                    uint32_t af[2][4];
+                    float t[2][NT][4];
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        mma_bf16(acc[x][m], af, pb[x][0], pb[x][1]);
-                        if (REST) mma_bf16(acc[x][m], af, pr[x][0], pr[x][1]);
-                    }
+                    for (int y = 0; y < 2; ++y)
+                        ldsm_x4_t(swz_addr(vbase, trow, 2 * (m0 + y) + ((lane >> 3) & 1)), af[y]);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) mma_bf16_new(t[y][x], af[y], pb[x][0], pb[x][1]);
+                    if (REST)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int x = 0; x < NT; ++x) mma_bf16(t[y][x], af[y], pr[x][0], pr[x][1]);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            acc[x][m0 + y][0] += t[y][x][0] + t[y][x][1];
+                            acc[x][m0 + y][1] += t[y][x][2] + t[y][x][3];
+                        }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            if constexpr (FLUSH)
-                if (k % kFlushTiles == kFlushTiles - 1) {
-                    // (a lane's own words: head c, dims gi and gi + 8 of every 16)
-                    const float f = mkept == -INFINITY ? 0.f : exp2f(mkept - mrun[0]);
-                    float* rw = red + (warp * 4 + c) * RED + gi;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const float a0 = acc[0][m][0] + acc[0][m][1], a1 = acc[0][m][2] + acc[0][m][3];
-                        rw[16 * m] = kept ? fmaf(rw[16 * m], f, a0) : a0;
-                        rw[16 * m + 8] = kept ? fmaf(rw[16 * m + 8], f, a1) : a1;
-                        acc[0][m][0] = acc[0][m][1] = acc[0][m][2] = acc[0][m][3] = 0.f;
-                    }
-                    kept = true;
-                    mkept = mrun[0];
-                }
         }
         // join the four warps' states, four heads at a time
 #pragma unroll
@@ -440,16 +438,10 @@ __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __gr
             float M = fmaxf(fmaxf(wm[flip][0][c], wm[flip][1][c]), fmaxf(wm[flip][2][c], wm[flip][3][c]));
             const float f = mrun[x] == -INFINITY ? 0.f : exp2f(mrun[x] - M);
             float* rw = red + (warp * 4 + c) * RED;
-            const float fk = mkept == -INFINITY ? 0.f : exp2f(mkept - mrun[x]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                float a0 = acc[x][m][0] + acc[x][m][1], a1 = acc[x][m][2] + acc[x][m][3];
-                if (FLUSH && kept) {
-                    a0 = fmaf(rw[16 * m + gi], fk, a0);
-                    a1 = fmaf(rw[16 * m + gi + 8], fk, a1);
-                }
-                rw[16 * m + gi] = a0 * f;
-                rw[16 * m + gi + 8] = a1 * f;
+                rw[16 * m + gi] = acc[x][m][0] * f;
+                rw[16 * m + gi + 8] = acc[x][m][1] * f;
             }
             bar_consumers();
             const int h = tid / (D / 4), d = tid % (D / 4) * 4;
@@ -760,8 +752,7 @@ template <int D, int PS, bool CLUSTER, bool REST>
 static int launch_range_bf16(const RangeArgs& a, int C, int cluster, const CUtensorMap* kmap, const CUtensorMap* vmap,
                              cudaStream_t stream)
 {
-    const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024 +
-                     (a.G == 8 || !REST ? 0 : D / 16 * 32 * (int)sizeof(uint2));
+    const int smem = 2 * kRangeStages * kRangeTile * D * 2 + 16 * (D + kRedPad) * 4 + 1024;
     const auto kern =
         a.G == 8 ? range_bf16_kernel<D, PS, 2, CLUSTER, REST> : range_bf16_kernel<D, PS, 1, CLUSTER, REST>;
     return launch_range_kernel(kern, C, kRangeThreads, cluster, smem, stream, *kmap, *vmap, a);
