@@ -631,6 +631,7 @@ int entmaxkv_prefix_softmax_decode(const entmaxkv_pool* pool, const float* q, in
     a.ps = pool->ps;
     a.row_tile = pool->dtype == ENTMAXKV_BF16 ? kPrefixRows : kPrefixRowsF32;
     a.block_tok = 64;
+    a.most = pool->dtype == ENTMAXKV_BF16 ? kPrefixMost : 1 << 30;   // fp32 sums are rounded
     a.C = lay.C;
     a.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
     a.gid = reinterpret_cast<int32_t*>(ws + lay.gid);

@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             if (lane == 0) mbar_arrive(&q_full);
         };
         int seg = 0, s_n = 0, k, n;
-        bool more = prefix_segment(a, w, k, n);
+        bool more = prefix_segment(a, w, k, n), again = false;   // again: the unit's partial holds segments before
+        float m_unit = -INFINITY, l_unit = 0.f;        // their maximum and sum
         if (more) {
             load_q();
             stage_q();
@@ -507,6 +508,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             // the next unit's query goes out before this unit's results: its first products run meanwhile
             const bool two = n > 1;
             prefix_advance(a, w);
+            const bool same = w.k > 0;
             more = prefix_segment(a, w, k, n);
             if (more) load_q();
             const bool ok = pfx_wait(&o_full, seg & 1, &dead, status);
@@ -517,8 +519,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
             // join the two accumulators: a warp takes D/4 columns of its rows
             if (ok && quad * 32 < rows) {
                 const float m0 = ml[0][row].x, m1 = ml[2][row].x;
-                const float M = fmaxf(m0, m1);
+                const float M = fmaxf(again ? m_unit : -INFINITY, fmaxf(m0, m1));
                 const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+                const float fu = !again || m_unit == -INFINITY ? 0.f : ex2(m_unit - M);
                 // partials lie [D / 4][rows] float4: the lanes of a warp store 512 consecutive bytes
                 float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * D) + row;
 #pragma unroll
@@ -537,13 +540,24 @@ __global__ void __launch_bounds__(kPfxThreads, 1) prefix_bf16_kernel(const __gri
                                 o[q] = __uint_as_float(x[e + q]) * f0;
                                 if (two) o[q] = fmaf(__uint_as_float(y[e + q]), f1, o[q]);
                             }
-                            dst[(c + e) / 4 * rows] = make_float4(o[0], o[1], o[2], o[3]);
+                            float4& to = dst[(c + e) / 4 * rows];
+                            if (again) {               // this thread's own words
+                                const float4 u = to;
+                                o[0] = fmaf(u.x, fu, o[0]);
+                                o[1] = fmaf(u.y, fu, o[1]);
+                                o[2] = fmaf(u.z, fu, o[2]);
+                                o[3] = fmaf(u.w, fu, o[3]);
+                            }
+                            to = make_float4(o[0], o[1], o[2], o[3]);
                         }
                 }
+                l_unit = (ml[0][row].y + ml[1][row].y) * f0 + (ml[2][row].y + ml[3][row].y) * f1 +
+                         (again ? l_unit * fu : 0.f);
+                m_unit = M;
                 if (row < rows && quarter == 0)
-                    reinterpret_cast<float2*>(a.part_ml)[part_row + row] =
-                        make_float2(M, (ml[0][row].y + ml[1][row].y) * f0 + (ml[2][row].y + ml[3][row].y) * f1);
+                    reinterpret_cast<float2*>(a.part_ml)[part_row + row] = make_float2(m_unit, l_unit);
             }
+            again = same;
             tc_fence_before();
             bar_softmax();                             // O and ml may come again
             ++seg;

@@ -24,7 +24,8 @@ def tolerance(d, adds, parts, cut):
       the query and the weights in `parts` bf16 parts: each off by at most 2^-9 / 2^9 per part, 1 / sqrt(3) of that
         rms (three parts: 2^-26, nothing beside the rest);
       weights: exp2 to two steps of 2^-23;
-      output: `cut` steps of the tensor cores between two rounded additions, and `adds` of those, 2^-25 rms each.
+      output: `cut` steps of the tensor cores, each cut off half a step of the whole sum, between two rounded
+        additions, and `adds` of those, 2^-25 rms each.
     Half as much again, since one output row is one sample."""
     scores = (parts * d / 16 if parts else math.sqrt(d)) * 2.0 ** -24
     split = math.sqrt(2 / 3) * 2.0 ** -18 if parts == 2 else 0.0
@@ -133,4 +134,18 @@ def test_own_tokens_of_one_cta(G, d, ps, around):
     o, lse = c.errors((0, 599))
     tol = tolerance(d, 313, 2, 1)
     print("own tokens G=%d d=%d: %.2e (tolerance %.2e), lse %.2e" % (G, d, o, tol, lse))
+    assert o <= tol and lse <= tol + 2.0 ** -20
+
+
+@pytest.mark.parametrize("around", [False, True])
+@pytest.mark.parametrize("G,n,d,ps", [(4, 2, 128, 64), (8, 16, 128, 64), (8, 40, 128, 16), (2, 3, 64, 16)])
+def test_long_prefixes_of_one_cta(G, n, d, ps, around):
+    """160 groups behind 100000 tokens: a CTA walks more than 1500 blocks of a unit (d 64, page 16: d / 16 score steps
+    a part).  Of each 128 blocks a set's accumulator takes 64, 8 steps each, into a sum that grows from nothing: 256
+    cut-offs of the whole sum on average."""
+    c = Long(160 * n, 100000, G, 1, d, ps, BF16, around, seed=n)
+    c.prefix(list(range(0, 160 * n + 1, n)), [100000] * 160)
+    o, lse = c.errors((0, n - 1, 71 * n + n // 2, 160 * n - 1))
+    tol = tolerance(d, 13, 2, 256)
+    print("prefix G=%d x %d d=%d: %.2e (tolerance %.2e), lse %.2e" % (G, n, d, o, tol, lse))
     assert o <= tol and lse <= tol + 2.0 ** -20
