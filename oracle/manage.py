@@ -68,7 +68,9 @@ def fork(s, src, dst):
             plan.append((a, b, None, 0))
             continue
         last = s.table[a][L // ps] if L % ps else -1
-        if 0 <= last < len(s.ref):
+        if last >= len(s.ref):
+            errors.add("bounds")
+        elif last >= 0:
             fresh = next(free, -1)
         if fresh == -1:
             errors.add("pages")

@@ -488,7 +488,7 @@ EKV_DEV int fork_need(const ForkArgs& a, int i, bool fine)
         if (fork_length_fine(a, L)) {
             if (L % a.ps == 0) return 0;
             const int e = a.page_table[(size_t)s * a.max_pages + L / a.ps];
-            return e >= 0 && e < a.num_phys;
+            if (e < a.num_phys) return e >= 0;
         }
     }
     report(a.status, ENTMAXKV_DEVICE_BOUNDS);
