@@ -132,6 +132,7 @@ def reserve(s, lens):
 def compact(s):
     errors = set()
     live = sum(r != 0 for r in s.ref)
+    used = [r != 0 for r in s.ref]
     holes = [p for p in range(live) if s.ref[p] == 0]
     movers = [p for p in range(live, len(s.ref)) if s.ref[p] != 0]
     to = dict(zip(movers, holes))
@@ -140,9 +141,8 @@ def compact(s):
         s.ref[b], s.ref[a] = s.ref[a], 0
     for row in s.table:
         for p, e in enumerate(row):
-            if e >= live:
-                if e in to:
-                    row[p] = to[e]
-                else:
-                    errors.add("bounds")
+            if e >= len(used) or e >= 0 and not used[e]:
+                errors.add("bounds")
+            elif e in to:
+                row[p] = to[e]
     return live, errors

@@ -255,7 +255,7 @@ struct PlanArgs {
     PlanHead* head;
     int32_t* free_ids;                   // ascending (compaction: the holes below the live count)
     int32_t* movers;                     // compaction: live pages at or above the live count, ascending
-    int32_t* rank;                       // compaction: a mover's position, -1 for a free page above the live count
+    int32_t* rank;                       // compaction: a mover's position, -1 for a free page, 0 for one that stays
     // rows that want pages, in order (fork: 0 or 1 each; reserve: any number)
     int rows;
     int32_t* want;                       // [rows] pages wanted
@@ -369,14 +369,15 @@ EKV_DEV void pages_plan(const PlanArgs& a, uint32_t* bits)
         const uint32_t m = bits[w];
         const int p = base + w * 32 + lane, lt = __popc(m & ((1u << lane) - 1)), n = min(32, end - (base + w * 32));
         if ((m >> lane) & 1) {
-            if (COMPACT && p >= all) {
-                a.movers[live_at + lt - below] = p;
-                a.rank[p] = live_at + lt - below;
+            if (COMPACT) {
+                const int k = live_at + lt - below;
+                if (p >= all) a.movers[k] = p;
+                a.rank[p] = max(k, 0);
             }
         } else if (lane < n) {
             const int f = free_at + lane - lt;
             if (p < hole_end && f < a.limit) a.free_ids[f] = p;
-            if (COMPACT && p >= all) a.rank[p] = -1;
+            if (COMPACT) a.rank[p] = -1;
         }
         live_at += __popc(m);
         free_at += n - __popc(m);
@@ -688,10 +689,10 @@ __global__ void __launch_bounds__(32) compact_apply_kernel(const PageBytes pb, i
     if (c == 0 && threadIdx.x == 0) *live = n_live;
     for (long long i = (long long)c * 32 + threadIdx.x; i < entries; i += (long long)ctas * 32) {
         const int e = page_table[i];
-        if (e < n_live) continue;
+        if (e < 0) continue;
         const int k = e < num_phys ? rank[e] : -1;
         if (k < 0) report(status, ENTMAXKV_DEVICE_BOUNDS);   // names no live page: left as it is
-        else page_table[i] = holes[k];
+        else if (e >= n_live) page_table[i] = holes[k];
     }
 }
 

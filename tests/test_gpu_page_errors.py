@@ -19,3 +19,23 @@ def test_fork_of_a_last_page_beyond_the_pool(rows):
     s.fork([1] + [3] * len(more), [4] + more)
     s.fork([1, 0] + [3] * len(more), [4, 5] + more)
     assert s.o.lens[4] == 33 and s.o.table[4][2] == -1 and s.o.lens[5] == 50
+
+
+@pytest.mark.parametrize("page", [1, 37])
+def test_compact_with_an_entry_of_a_free_page(page):
+    """A table names a page whose count is zero: below the pages in use, where another page moves to, and above."""
+    s = Both(40, 3, 20)
+    s.reserve([300, 260, 0])
+    s.set_lens([300, 260, 0])
+    s.free([0])
+    s.reserve([40, 260, 20])
+    s.set_lens([40, 260, 20])
+    assert s.o.ref[page] == (page == 1)
+    if page == 1:
+        s.ref[1] = s.o.ref[1] = 0             # row 0's second page
+        assert s.o.table[0][1] == 1
+    else:
+        s.table[0, 1] = s.o.table[0][1] = page
+        s.ref[1] = s.o.ref[1] = 0
+    s.compact()
+    s.free(None)
