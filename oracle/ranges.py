@@ -32,8 +32,9 @@ def error_bound(q, keys, vals, scale, split):
     """(bound on |o - o_ref| [G, d], bound on |lse - lse_ref| [G]) for fp32 sums.
 
     split: the query and the weights enter their products as a bf16 high and low
-    part.  Each part rounds by half a step (2^-9 of the value), so hi + lo is
-    the value to 2^-18.  Otherwise they enter as fp32 (2^-24).  With
+    part (at least).  Of a value in [1, 2) the high part leaves a rest of at most
+    half a step, 2^-8, and a step of a rest below 2^-8 is at most 2^-16: hi + lo
+    is the value to 2^-17.  Otherwise they enter as fp32 (2^-24).  With
     A = scale sum_d |q_d k_d|:
       dx  = A (r + d 2^-23) + 2^-22 (|x| + max |x|)
             the query's rounding r, the fp32 sum over d (one step of 2^-23 a
@@ -46,7 +47,7 @@ def error_bound(q, keys, vals, scale, split):
     n, d = keys.shape
     if n == 0:
         return np.zeros((q.shape[0], vals.shape[1])), np.zeros(q.shape[0])
-    r = 2.0 ** -18 if split else 2.0 ** -24
+    r = 2.0 ** -17 if split else 2.0 ** -24
     x = scale * (q @ keys.T)
     A = scale * (np.abs(q) @ np.abs(keys).T)
     dx = A * (r + d * 2.0 ** -23) + 2.0 ** -22 * (np.abs(x) + np.abs(x).max(axis=1, keepdims=True))

@@ -411,9 +411,10 @@ static PrefixLayout prefix_layout(int B, int H_q, int H_kv, int d)
 
 // Below this many bytes of keys and values (all sequences at the longest that
 // the page table holds) a prefix call reads them for each sequence: that takes
-// two launches instead of four, 11 us less, in which HBM and L2 deliver more
-// than this.  Measured on 4 sequences behind 1000 tokens (21 MB): 16 us
-// against 27; on 32 behind 4 x 16384 (1.3 GB): 210 against 98.
+// one or two launches instead of four, 11 us less, in which HBM and L2 deliver
+// more than this.  Measured on 4 sequences behind 1000 tokens: 10.9 us with a
+// table of their length (21 MB), 23.6 with one of 2048 pages a row, which goes
+// the other way; on 32 behind 4 x 16384 (1.3 GB): 210 against 98.
 constexpr double kPrefixLeastBytes = 64 << 20;
 
 // ------------------------------------------------------------------ pages

@@ -463,7 +463,7 @@ struct ForkArgs {
     int n;
     const PlanHead* head;
     const int32_t* free_ids;
-    int32_t* want;                       // [n] 1 where a fork needs a page of its own, -1 where it is refused
+    int32_t* want;                       // [n] 1 where a fork needs a page of its own (0 where it is refused)
     const int32_t* at;
     int32_t* status;
 };

@@ -270,16 +270,19 @@ EKV_DEV uint32_t bf16x2(float2 v)
 //   warp 17      issues the products S = (Q_hi + Q_lo) K^T and
 //                O += (P_hi + P_lo) V, with Q and P read from tensor memory, so
 //                that shared memory feeds one operand only.
-// Query and weights enter as a bf16 high and low part (2^-18 of relative error
-// each), which doubles the products: at 128 rows 1024 tensor cycles a block
-// stand against ~1300 in which HBM delivers its 32 KB, so the bytes still
-// bound the time; more rows than a tile's 128 make the products bound it.  O is
-// rescaled only when the maximum grew by more than 2^8, which keeps every
-// weight in range and rescaling rare.
+// Query and weights enter as a bf16 high and low part (2^-17 of relative error
+// each at most, 3.4e-6 rms together), which doubles the products: at 128 rows
+// 1024 tensor cycles a block, where HBM takes ~1300 cycles of a full clock to
+// deliver its 32 KB.  At full clock the bytes bound the time then; when the power
+// cap lowers the clock, and with more rows than a tile's 128, the products do.
+// A third part would need more tensor memory than there is beside two
+// accumulators.  O is rescaled only when the maximum grew by more than 2^8, which
+// keeps every weight in range and rescaling rare.
 //
 // Measured (the kernel alone, profiled; 8 kv heads of 128 dims): 128 rows behind
-// 131072 tokens 107 us, 5.0 TB/s; 384 rows behind 32809 84 us, the tensor pipe busy
-// 64% of the time (1275 cycles a block, of which the product warp waits a fifth).
+// 131072 tokens 93 to 107 us, 5.8 to 5.0 TB/s, by the clock that the power cap
+// leaves; 384 rows behind 32809 72 to 84 us (84 at 1.6 GHz, the tensor pipe busy 64%
+// of the time: 1275 cycles a block, of which the product warp waits a fifth).
 // With blocks of 128 tokens and Q in shared memory the latter took 118 us.
 constexpr int kPfxRows = 128, kPfxTok = 64;
 constexpr int kPfxSoft = 16;             // softmax warps

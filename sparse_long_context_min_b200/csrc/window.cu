@@ -133,7 +133,7 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // block barrier stands between a tile's arrival and its release.  The query is
 // the B operand of the score product, its result's layout is turned in registers
 // (movmatrix) into the B operand of V^T P.  Both enter in bf16 parts: one would
-// leave 2^-9 of relative error, two 2^-18, three 2^-26.  The first two are columns
+// leave 2^-8 of relative error, two 2^-17, three 2^-26.  The first two are columns
 // 2h and 2h + 1 of one product, the third is column 2h of a second into the same
 // accumulators.  A window takes three (REST): that doubles the products, which
 // the bytes hide but for 1.5% (64 sequences of 8192 + 64 tokens: 293.7 -> 298.1
@@ -144,8 +144,8 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // 65536 tokens of values around 1).  So the products of a warp's 16 tokens start
 // from zero and are added to the output by rounded adds (2.5e-7 there, as plain
 // fp32 sums have).  Two slices of 16 dims at a time, so that no product waits for
-// the one before: 64 windows of 8256 tokens 302 us at 4 heads a group, 331 at 8
-// (one slice at a time 367).
+// the one before: 64 windows of 8256 tokens 302 us at 4 heads a group; at 8 331 us
+// under the power cap (one slice at a time 367), 309 at full clock.
 template <int D, int PS, int NT, bool CLUSTER, bool REST>
 __global__ void __launch_bounds__(kRangeThreads, 2) range_bf16_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                       const __grid_constant__ CUtensorMap vmap,

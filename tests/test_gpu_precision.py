@@ -21,14 +21,15 @@ def tolerance(d, adds, parts, cut):
     """Relative 2-norm error for scores of one nat rms.  Independent errors join as the root of their squares:
       scores: the product's parts * d / 16 steps (fp32 caches: d roundings) of the tensor cores each cut off half
         a step of 2^-23 on average, all to the same side;
-      the query and the weights in `parts` bf16 parts: each off by at most 2^-9 / 2^9 per part, 1 / sqrt(3) of that
-        rms (three parts: 2^-26, nothing beside the rest);
+      the query and the weights in two bf16 parts: of a value in [1, 2) the first leaves a rest within 2^-8, whose
+        rounding lies within 2^-8 2^e, e the rest's exponent, and 4^e is 2^-16 / 7 on average: 2^-16 / sqrt(21) rms,
+        1 / sqrt(2) of that relative to the value, and two such errors (three parts: 2^-26, nothing beside the rest);
       weights: exp2 to two steps of 2^-23;
       output: `cut` steps of the tensor cores, each cut off half a step of the whole sum, between two rounded
         additions, and `adds` of those, 2^-25 rms each.
     Half as much again, since one output row is one sample."""
     scores = (parts * d / 16 if parts else math.sqrt(d)) * 2.0 ** -24
-    split = math.sqrt(2 / 3) * 2.0 ** -18 if parts == 2 else 0.0
+    split = 2.0 ** -16 / math.sqrt(21) if parts == 2 else 0.0
     return 1.5 * math.sqrt(scores ** 2 + split ** 2 + 2.0 ** -44 + (cut * 2.0 ** -24) ** 2 + adds * 2.0 ** -50)
 
 
@@ -112,7 +113,7 @@ def test_window_of_one_cta(G, d, ps, around):
 
 @pytest.mark.parametrize("G,dtype", [(4, BF16), (8, BF16), (4, F32)])
 def test_short_window(G, dtype):
-    """The bf16 parts of the query and the weights are three: with two the error is 2^-18."""
+    """The bf16 parts of the query and the weights are three: with two the error is 3.3e-6."""
     c = Long(64, 5000, G, 2, 128, 64, dtype, False, seed=3)
     c.window(1020, 8)
     c.L, tokens = 5000, np.r_[0:8, 3980:5000]
