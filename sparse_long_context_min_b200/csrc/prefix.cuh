@@ -55,12 +55,12 @@ constexpr int kPrefixTurn = 6;
 // Blocks that the bf16 kernel's tensor cores sum by themselves (PrefixArgs::most).
 // They cut every step off, always to the same side: 2e-7 of a sum of values of one
 // sign a block.  A segment's result is added to the unit's partial by rounded
-// adds, so that long shares lose no more than one of 128 blocks (1.7e-5; 4.4e-4
-// at 2048 blocks otherwise).  Its end costs about as much as its start: measured at 20 x 16
-// sequences behind 65536 tokens 4% (1130 -> 1178 us); shares of 111 blocks (32
-// sequences behind 131072 tokens, one kv head's 2048 blocks for 18 CTAs) stay whole.  With
-// segments of 64 those take 142 us for 136.6, with 32 152; their error falls
-// from 9.0e-6 to 5.8e-6 and 4.3e-6, of which the two bf16 parts make 3.6e-6.
+// adds, so that long shares lose no more than one of 128 blocks does (1.7e-5; 4.4e-4
+// at 2048 blocks otherwise).  A segment's end costs about as much as a unit's start:
+// 4% at 20 x 16 sequences behind 65536 tokens (1130 -> 1178 us).  Shares of 111 blocks
+// (32 sequences behind 131072 tokens, one kv head's 2048 blocks for 18 CTAs) are one
+// segment: 136.6 us; with segments of 64 blocks 142, of 32 152, at errors of 9.0e-6,
+// 5.8e-6 and 4.3e-6, of which the two bf16 parts make 3.6e-6.
 constexpr int kPrefixMost = 128;
 
 EKV_DEV int prefix_len(const PrefixGroup& G) { return G.blocks + kPrefixTurn; }

@@ -138,7 +138,9 @@ EKV_DEV void range_note_span(const RangeArgs& a, const RangeWalk& w, int u, int 
 // accumulators.  A window takes three (REST): that doubles the products, which
 // the bytes hide but for 1.5% (64 sequences of 8192 + 64 tokens: 293.7 -> 298.1
 // us), and brings the error of 1028 tokens from 3.2e-6 to 3.6e-7 (2-norms).  The
-// tokens behind a shared prefix take two parts, as the prefix itself does (3.5e-6).
+// tokens behind a shared prefix take two parts, as the prefix itself does (3.5e-6):
+// three would cost 4 x 8 sequences behind 16384 tokens 4% (102.3 -> 106.5 us), at 8
+// heads a group 11%, for sums of which the prefix makes most.
 // The tensor cores cut their sums off and do not round them, always to the same
 // side: left in their accumulators, a sum loses 8e-8 of itself a tile (8e-5 at
 // 65536 tokens of values around 1).  So the products of a warp's 16 tokens start
